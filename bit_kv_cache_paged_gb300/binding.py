@@ -35,6 +35,17 @@ class OscarConfig(ctypes.Structure):
                 ("v_rot_absorbed", c_i32), ("flags", c_i32)]
 
 
+class OscarRopeConfig(ctypes.Structure):
+    _fields_ = [("rot_dim", c_i32), ("interleaved", c_i32), ("scaling", c_i32), ("original_len", c_i32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class OscarRope(ctypes.Structure):
+    _fields_ = [("rot_dim", c_i32), ("interleaved", c_i32), ("amplitude", ctypes.c_float), ("reserved", c_i32),
+                ("turns", ctypes.c_uint64 * 64)]
+
+
 class OscarPoolStats(ctypes.Structure):
     _fields_ = [("int2_pages_used", c_i64), ("int2_pages_free", c_i64), ("sink_pages_used", c_i32),
                 ("seqs_active", c_i32), ("bf16_bytes_per_token", c_i64), ("int2_bytes_per_token", c_i64)]
@@ -61,6 +72,16 @@ _SIGS = {
     "oscar_bf16_pack": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_vp, c_vp]),
     "oscar_bf16_decode": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_i64, c_vp, c_i32, c_vp, c_vp, c_vp,
                                   c_sz, c_vp, c_vp, c_vp]),
+    "oscar_chunk_workspace_bytes": (c_sz, [c_vp]),
+    "oscar_chunk_attend": (c_i32, [c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "oscar_bf16_chunk_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32, c_i32]),
+    "oscar_bf16_chunk": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_i64, c_vp, c_i32, c_vp, c_vp, c_vp, c_i64,
+                                 c_vp, c_sz, c_vp, c_vp, c_vp]),
+    "oscar_bf16_copy_pages": (c_i32, [c_i32, c_i32, c_sz, c_vp, c_vp, c_i64, ctypes.POINTER(c_i32),
+                                      ctypes.POINTER(c_i32), c_i32, c_vp]),
+    "oscar_rope_init": (c_i32, [ctypes.POINTER(OscarRopeConfig), ctypes.POINTER(OscarRope)]),
+    "oscar_rope_apply": (c_i32, [ctypes.POINTER(OscarRope), c_i32, c_vp, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp,
+                                 c_i64, c_vp, c_i64, c_vp]),
     "oscar_step_graph": (c_i32, [c_vp, c_vp, c_vp, c_sz, c_vp, c_sz, c_vp, c_vp, c_vp, c_sz, c_vp]),
     "oscar_decode_merge_noalloc": (c_i32, [c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp]),
     "oscar_check": (c_i32, [c_vp, c_vp, ctypes.POINTER(c_u32)]),
@@ -205,6 +226,53 @@ def oscar_bf16_decode(num_q_heads, num_kv_heads, n_seqs, max_len, k_pages, v_pag
                                                         _ptr(v_pages), n_pages_total, _ptr(page_table),
                                                         max_pages_per_seq, _ptr(lengths), _ptr(q), _ptr(partials),
                                                         partials_bytes, _ptr(out), _ptr(err), stream))
+
+
+def oscar_bf16_chunk_workspace_bytes(num_q_heads, num_kv_heads, n_seqs, n_tokens) -> int:
+    return lib().oscar_bf16_chunk_workspace_bytes(num_q_heads, num_kv_heads, n_seqs, n_tokens)
+
+
+def oscar_bf16_chunk(num_q_heads, num_kv_heads, n_seqs, n_tokens, k_pages, v_pages, n_pages_total, page_table,
+                     max_pages_per_seq, lengths, cu_tokens, q, q_token_stride, workspace, workspace_bytes, out, err,
+                     stream):
+    _check("oscar_bf16_chunk", lib().oscar_bf16_chunk(num_q_heads, num_kv_heads, n_seqs, n_tokens, _ptr(k_pages),
+                                                      _ptr(v_pages), n_pages_total, _ptr(page_table),
+                                                      max_pages_per_seq, _ptr(lengths), _ptr(cu_tokens), _ptr(q),
+                                                      q_token_stride, _ptr(workspace), workspace_bytes, _ptr(out),
+                                                      _ptr(err), stream))
+
+
+def oscar_bf16_copy_pages(num_kv_heads, n_layers, layer_stride, k_pages, v_pages, n_pages_total, src, dst, stream):
+    """src, dst: host sequences of page ids (pairs)."""
+    if len(src) != len(dst):
+        raise OscarError("oscar_bf16_copy_pages", OSCAR_EINVAL)
+    n = len(src)
+    a = (c_i32 * n)(*[int(x) for x in src])
+    b = (c_i32 * n)(*[int(x) for x in dst])
+    _check("oscar_bf16_copy_pages", lib().oscar_bf16_copy_pages(num_kv_heads, n_layers, layer_stride, _ptr(k_pages),
+                                                                _ptr(v_pages), n_pages_total, a, b, n, stream))
+
+
+def oscar_rope_init(cfg: OscarRopeConfig) -> OscarRope:
+    out = OscarRope()
+    _check("oscar_rope_init", lib().oscar_rope_init(ctypes.byref(cfg), ctypes.byref(out)))
+    return out
+
+
+def oscar_rope_apply(rope, n_tokens, positions, num_q_heads, q, q_stride, q_out, q_out_stride, num_k_heads, k,
+                     k_stride, k_out, k_out_stride, stream):
+    _check("oscar_rope_apply", lib().oscar_rope_apply(ctypes.byref(rope), n_tokens, _ptr(positions), num_q_heads,
+                                                      _ptr(q), q_stride, _ptr(q_out), q_out_stride, num_k_heads,
+                                                      _ptr(k), k_stride, _ptr(k_out), k_out_stride, stream))
+
+
+def oscar_chunk_workspace_bytes(pool) -> int:
+    return lib().oscar_chunk_workspace_bytes(pool)
+
+
+def oscar_chunk_attend(pool, layer, q, k_new, v_new, workspace, out, stream):
+    _check("oscar_chunk_attend", lib().oscar_chunk_attend(pool, layer, _ptr(q), _ptr(k_new), _ptr(v_new),
+                                                          _ptr(workspace), _ptr(out), stream))
 
 
 def oscar_partials_bytes(pool, n_seqs) -> int:

@@ -121,6 +121,10 @@ cudaError_t launch_decode_bf16(const DevPool& P, const StepDims& S, int layer, c
                                float* partials, cudaStream_t s);
 cudaError_t launch_merge(const DevPool& P, const StepDims& S, int layer, const float* partials_int2,
                          const float* partials_bf16, float* out, cudaStream_t s);
+// Attention of new tokens over a cache (chunk.cu). workspace: chunk_workspace_bytes() bytes.
+size_t chunk_workspace_bytes(int hg, int64_t n_tokens);
+cudaError_t launch_chunk_pool(const DevPool& P, const StepDims& S, int layer, const void* q, const void* k_new,
+                              const void* v_new, void* workspace, void* out, cudaStream_t s);
 cudaError_t launch_debug_rotate(const DevPool& P, int layer, int head, int kv, const void* x, int n,
                                 float* out, cudaStream_t s);
 cudaError_t launch_debug_read_int2(const DevPool& P, int seq, int layer, int head, int pos0, int n,
@@ -150,6 +154,7 @@ struct PoolStepView {
   bool in_step, host_only;
   int device;                      // the device the pool's memory lives on
   int64_t* launch_count;
+  const uint8_t* appended;         // per layer: append_and_demote was called in this step
 };
 void pool_step_view(oscar_pool* p, PoolStepView* v);
 

@@ -111,6 +111,7 @@ struct oscar_pool {
   bool stepped = false;  // a step has begun since creation (the codebook is fixed from then on)
   std::vector<StepSeq> step;
   StepDims dims{};
+  std::vector<uint8_t> appended;  // per layer: append_and_demote was called in this step
   // pinned staging for step uploads (double-buffered)
   uint8_t* pinned[2] = {nullptr, nullptr};
   size_t pinned_bytes = 0;
@@ -281,6 +282,7 @@ void oscar::pool_step_view(oscar_pool* p, PoolStepView* v) {
   v->host_only = p->host_only;
   v->device = p->device;
   v->launch_count = &p->launch_count;
+  v->appended = p->appended.data();
 }
 
 extern "C" {
@@ -311,6 +313,7 @@ oscar_status oscar_pool_create(const oscar_config* cfg, void* dev_arena, size_t 
   p->sink_ref.assign(p->lay.max_sink_pages, 0);
   for (int32_t i = p->lay.max_sink_pages - 1; i >= 0; --i) p->sink_free.push_back(i);
   p->step.reserve(cfg->max_seqs);
+  p->appended.assign(cfg->num_layers, 0);
   if (p->host_only) {
     if (dev_arena || arena_bytes || U_k || U_v || clip_k || clip_v) {
       delete p;
@@ -575,6 +578,7 @@ oscar_status oscar_step_begin(oscar_pool* p, const int32_t* seq_ids, const int32
   }
   p->in_step = true;
   p->stepped = true;
+  std::fill(p->appended.begin(), p->appended.end(), (uint8_t)0);
   if (p->host_only) return OSCAR_OK;
 
   // upload: step description + page-table scatter list through pinned staging
@@ -614,6 +618,7 @@ oscar_status oscar_append_and_demote(oscar_pool* p, int32_t layer, const void* k
   if (p->dims.total_new > 0 && (!k_new || !v_new)) return OSCAR_EINVAL;
   if (!aligned16(k_new) || !aligned16(v_new)) return OSCAR_EINVAL;  // the kernels copy 16-byte chunks
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  p->appended[layer] = 1;
   oscar_status r = OSCAR_OK;
   if (p->dims.total_dem > 0)
     r = timed_launch(p, OSCAR_KERNEL_DEMOTE, st, [&] { return launch_demote(p->P, p->dims, layer, k_new, v_new, st); });
@@ -629,6 +634,29 @@ oscar_status oscar_rotate_q(oscar_pool* p, int32_t layer, const void* q, float* 
   if (p->host_only) return OSCAR_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return timed_launch(p, OSCAR_KERNEL_ROTATE_Q, st, [&] { return launch_rotate_q(p->P, p->dims, layer, q, q_rot, st); });
+}
+
+size_t oscar_chunk_workspace_bytes(const oscar_pool* p) {
+  if (!p || !p->in_step || p->host_only) return 0;
+  return chunk_workspace_bytes(p->hg, p->dims.total_new);
+}
+
+oscar_status oscar_chunk_attend(oscar_pool* p, int32_t layer, const void* q, const void* k_new, const void* v_new,
+                                void* workspace, void* out, void* stream) {
+  if (!p || layer < 0 || layer >= p->cfg.num_layers) return OSCAR_EINVAL;
+  if (!p->in_step) return OSCAR_ESTATE;
+  if (p->host_only) return OSCAR_EINVAL;
+  if (p->appended[layer]) return OSCAR_ESTATE;  // the ring no longer holds the rows before the step
+  if (p->dims.total_new == 0) return OSCAR_OK;
+  if (!q || !k_new || !v_new || !workspace || !out) return OSCAR_EINVAL;
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(workspace) || !aligned16(out)) return OSCAR_EINVAL;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cuda_fail(cudaErrorUnknown);
+  if (dev != p->device) return OSCAR_EINVAL;
+  const cudaError_t e = launch_chunk_pool(p->P, p->dims, layer, q, k_new, v_new, workspace, out, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  p->launch_count++;
+  return OSCAR_OK;
 }
 
 size_t oscar_partials_bytes(const oscar_pool* p, int32_t n_seqs) {
@@ -789,6 +817,7 @@ oscar_status oscar_step_graph(oscar_pool* p, const void* k_new, const void* v_ne
     std::memcpy(&p->graph_key, &key, sizeof(key));
     p->graph_captures++;
   }
+  std::fill(p->appended.begin(), p->appended.end(), (uint8_t)1);
   const cudaError_t e = cudaGraphLaunch(p->graph_exec, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
   p->launch_count += p->graph_kernels;

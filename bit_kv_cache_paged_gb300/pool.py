@@ -37,6 +37,7 @@ class Pool:
         self.group_size = group_size
         self.host_only = host_only
         self.n_seqs = 0
+        self.total_new = 0
         self.handle = None
         self._partials = None
         if host_only:
@@ -130,6 +131,23 @@ class Pool:
         q_rot = self.rotate_q(layer, q)
         part = self.decode(layer, q, q_rot)
         return self.merge(layer, part)
+
+    def chunk_attend(self, layer, q, k_new, v_new, out=None):
+        """Attention of the step's new tokens (bf16 q [Σn_new, Hq, 128], k_new / v_new [Σn_new, Hkv, 128]) over the
+        cache as it stood before the step and the chunk itself, causal; between step_begin and this layer's
+        append_and_demote. Returns bf16 [Σn_new, Hq, 128]."""
+        T = self.total_new
+        _need(q, torch.bfloat16, (T, self.Hq, HEAD_DIM), "q")
+        _need(k_new, torch.bfloat16, (T, self.Hkv, HEAD_DIM), "k_new")
+        _need(v_new, torch.bfloat16, (T, self.Hkv, HEAD_DIM), "v_new")
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        _need(out, torch.bfloat16, q.shape, "out")
+        # a buffer of the call's own: torch's allocator keeps it apart from calls on other streams
+        # and from captured graphs
+        workspace = torch.empty(max(B.oscar_chunk_workspace_bytes(self.handle), 16), dtype=torch.uint8, device=q.device)
+        B.oscar_chunk_attend(self.handle, layer, q, k_new, v_new, workspace, out, _stream())
+        return out
 
     def step_graph(self, k_new, v_new, q, q_rot=None, out=None):
         """Every layer's append_and_demote + rotate_q + decode + merge as one CUDA graph launch.

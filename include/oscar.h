@@ -219,6 +219,25 @@ oscar_status oscar_step_graph(oscar_pool* pool, const void* k_new_bf16, const vo
                               float* q_rot, void* partials, float* out, size_t out_layer_stride,
                               void* stream);
 
+/* Attention of the current step's new tokens (chunked prefill, drafted tokens, mixed batches) for one
+ * layer, over the cache as it stands before the step and the step's own rows: between
+ * oscar_step_begin and this layer's oscar_append_and_demote (OSCAR_ESTATE once that has been
+ * called in the step). Token j of batch index i has position L_old + j and sees the sink, the INT2
+ * history [64, F_old) (as in oscar_decode: codes restored with scale and zero point, compared in the
+ * rotated basis, values un-rotated by R_V^T unless v_rot_absorbed), the recent rows [F_old, L_old)
+ * and the chunk's tokens 0 .. j, all but the history in BF16. A step of single tokens therefore sees
+ * the token that leaves the recent window still in BF16, where oscar_decode (after the demote) sees
+ * it in INT2.
+ *   q: dev bf16 [sum(n_new)][num_q_heads][128]; k_new, v_new: dev bf16 [sum(n_new)][num_kv_heads][128],
+ *   rows as for oscar_append_and_demote; out: dev bf16, shape of q; workspace: dev scratch of
+ *   oscar_chunk_workspace_bytes(pool) bytes (calls that may overlap need one each). All 16-byte aligned.
+ * Runs on the pool's device, which must be current (OSCAR_EINVAL). Errors found by the kernels
+ * (a bad page id, a bounded wait) surface from oscar_check. */
+size_t oscar_chunk_workspace_bytes(const oscar_pool* pool);
+oscar_status oscar_chunk_attend(oscar_pool* pool, int32_t layer, const void* q_bf16,
+                                const void* k_new_bf16, const void* v_new_bf16, void* workspace,
+                                void* out_bf16, void* stream);
+
 /* Bytes of partials scratch that oscar_decode needs for the current step (n_seqs must equal the
  * step's batch): a bound that depends only on the batch size and the pool, so one buffer serves
  * every step of a batch. Returns 0 outside a step or on a mismatch. */
@@ -315,6 +334,91 @@ oscar_status oscar_bf16_decode(int32_t num_q_heads, int32_t num_kv_heads, int32_
                                int32_t max_pages_per_seq, const int32_t* lengths,
                                const void* q_bf16, void* partials, size_t partials_bytes, float* out,
                                uint32_t* err, void* stream);
+
+/* Attention of a chunk of new tokens over the BF16 pages (chunked prefill, verification of drafted
+ * tokens, mixed batches). The chunk's K and V rows are in the pages already. Sequence i owns rows
+ * cu_tokens[i] .. cu_tokens[i+1]-1 of q and out; they are its last n_i tokens, so row t of them has
+ * position lengths[i] - n_i + t and sees the keys 0 .. that position. A row of negative position
+ * sees nothing and gets zeros; rows of q outside every sequence are not read into any result and
+ * their out rows are left as they were.
+ *   q: dev bf16 [n_tokens][num_q_heads][128], token t at q + t * q_token_stride elements (a
+ *     multiple of 8, at least num_q_heads * 128); out: dev bf16 [n_tokens][num_q_heads][128].
+ *   Hq / Hkv must be 1, 2, 4, 8 or 16. page_table, pages, n_pages_total as above; entries past a
+ *     sequence's last page are not read, slots past its length may hold anything.
+ *   lengths, cu_tokens: dev int32 [n_seqs] and [n_seqs + 1] (ascending, at most n_tokens); they are
+ *     read when the kernels run, so a captured call follows their contents. A length above
+ *     64 * max_pages_per_seq, or a bad page id, sets OSCAR_DEVERR_PAGE in *err (then the call's
+ *     outputs are not valid; nothing outside the buffers is read or written).
+ *   workspace: dev scratch of oscar_bf16_chunk_workspace_bytes(...) bytes, 16-byte aligned; calls
+ *     that may overlap in time need one each.
+ * Scores, softmax statistics and sums are fp32; the softmax weights enter the value product in
+ * bf16. Asynchronous on `stream`; allocates nothing. */
+size_t oscar_bf16_chunk_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t n_seqs,
+                                        int32_t n_tokens);
+oscar_status oscar_bf16_chunk(int32_t num_q_heads, int32_t num_kv_heads, int32_t n_seqs,
+                              int32_t n_tokens, const void* k_pages, const void* v_pages,
+                              int64_t n_pages_total, const int32_t* page_table,
+                              int32_t max_pages_per_seq, const int32_t* lengths,
+                              const int32_t* cu_tokens, const void* q_bf16, int64_t q_token_stride,
+                              void* workspace, size_t workspace_bytes, void* out_bf16, uint32_t* err,
+                              void* stream);
+
+/* Copy whole pages of the BF16-only cache: for every layer l < n_layers and m < n, page dst[m] of
+ * K and of V becomes page src[m] (all KV heads). Fork of a sequence (its last, partly filled page;
+ * the full ones are shared through the page table) and compaction. k_pages, v_pages: dev bf16
+ * [n_pages_total][num_kv_heads][64][128], layer l at + l * layer_stride bytes (a multiple of 16, at
+ * least one layer's pages when n_layers > 1). src, dst: host int32 [n], read before the call
+ * returns; a page may be copied to several places, but no page may be written twice or be both
+ * read and written (OSCAR_EINVAL, as for an id out of range, and nothing is launched).
+ * Asynchronous on `stream`. */
+oscar_status oscar_bf16_copy_pages(int32_t num_kv_heads, int32_t n_layers, size_t layer_stride,
+                                   void* k_pages, void* v_pages, int64_t n_pages_total,
+                                   const int32_t* src, const int32_t* dst, int32_t n, void* stream);
+
+/* ---- Rotary positions ---------------------------------------------------------------------
+ * Queries and keys enter the caches with their positions applied. For pair j of the first rot_dim
+ * dims and a token at position p, the angle is p * w_j with w_j = base^(-2j / rot_dim) and
+ *   (x_a, x_b) -> amplitude * (x_a cos - x_b sin, x_b cos + x_a sin),
+ * pairs (a, b) = (j, j + rot_dim/2), or (2j, 2j + 1) when interleaved. The other dims are copied. */
+#define OSCAR_ROPE_NONE 0    /* w_j as above */
+#define OSCAR_ROPE_LINEAR 1  /* w_j / factor (positions interpolated) */
+#define OSCAR_ROPE_BASE 2    /* base * factor^(rot_dim / (rot_dim - 2)) in the place of base */
+#define OSCAR_ROPE_RAMP 3    /* w_j / factor * r_j + w_j * (1 - r_j), where r_j rises linearly from 0 to 1
+                                between the pairs that turn beta_fast and beta_slow times within
+                                original_len positions (floor and ceiling of their indices); the
+                                frequency schedule of YaRN (Peng et al., 2023) */
+typedef struct oscar_rope_config {
+  int32_t rot_dim;      /* multiple of 16, 16 .. 128 */
+  int32_t interleaved;  /* 0: halves, 1: neighbours */
+  int32_t scaling;      /* OSCAR_ROPE_* */
+  int32_t original_len; /* RAMP: >= 1 */
+  double base;          /* > 1 */
+  double factor;        /* >= 1 (1 without scaling) */
+  double beta_fast, beta_slow; /* RAMP: beta_fast >= beta_slow > 0 */
+  double amplitude;     /* > 0; 0 takes the scaling's own: 0.1 ln(factor) + 1 for RAMP, else 1 */
+} oscar_rope_config;
+
+/* What the kernel needs of a configuration, filled by oscar_rope_init and passed by the caller. */
+typedef struct oscar_rope {
+  int32_t rot_dim, interleaved;
+  float amplitude;
+  int32_t reserved;
+  uint64_t turns[64];   /* w_j / 2 pi in units of 2^-64 of a turn */
+} oscar_rope;
+
+oscar_status oscar_rope_init(const oscar_rope_config* cfg, oscar_rope* out);
+
+/* Rotate n_tokens rows of q and of k (either may be NULL with 0 heads) in one launch: token t of q is
+ * [num_q_heads][128] bf16 at q + t * q_stride elements, and goes to q_out + t * q_out_stride; k
+ * likewise. Pointers are dev and 16-byte aligned, strides multiples of 8 elements, at least
+ * heads * 128. positions: dev int32 [n_tokens] (negative ones turn the other way). q_out may be q
+ * with the same stride (in place); other overlaps of an input with an output give OSCAR_EINVAL where
+ * they are of the same tensor, and are the caller's to avoid between q and k. Angles are reduced
+ * exactly (integer turns), so far positions keep full precision. Asynchronous on `stream`. */
+oscar_status oscar_rope_apply(const oscar_rope* rope, int32_t n_tokens, const int32_t* positions,
+                              int32_t num_q_heads, const void* q, int64_t q_stride, void* q_out,
+                              int64_t q_out_stride, int32_t num_k_heads, const void* k,
+                              int64_t k_stride, void* k_out, int64_t k_out_stride, void* stream);
 
 /* ---- Parity hooks (synchronous on `stream`; for tests, not for the hot path) -------------- */
 
