@@ -89,6 +89,7 @@ _SIGS = {
     "oscar_pool_get_stats": (c_i32, [c_vp, ctypes.POINTER(OscarPoolStats)]),
     "oscar_debug_rotate_rows": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp]),
     "oscar_debug_read_int2": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "oscar_debug_write_int2": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
     "oscar_debug_read_bf16": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp]),
     "oscar_debug_timeout_selftest": (c_i32, [c_vp, c_vp]),
     "oscar_debug_set_page_entry": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_vp]),
@@ -312,6 +313,11 @@ def oscar_debug_rotate_rows(pool, layer, kv_head, kv, x, n, out, stream):
 def oscar_debug_read_int2(pool, seq_id, layer, kv_head, pos0, n, codes_k, sz_k, codes_v, sz_v, stream):
     _check("oscar_debug_read_int2", lib().oscar_debug_read_int2(pool, seq_id, layer, kv_head, pos0, n, _ptr(codes_k),
                                                                 _ptr(sz_k), _ptr(codes_v), _ptr(sz_v), stream))
+
+
+def oscar_debug_write_int2(pool, seq_id, layer, kv_head, pos0, n, codes_k, sz_k, codes_v, sz_v, stream):
+    _check("oscar_debug_write_int2", lib().oscar_debug_write_int2(pool, seq_id, layer, kv_head, pos0, n, _ptr(codes_k),
+                                                                  _ptr(sz_k), _ptr(codes_v), _ptr(sz_v), stream))
 
 
 def oscar_debug_read_bf16(pool, seq_id, layer, kv_head, pos0, n, k_out, v_out, stream):

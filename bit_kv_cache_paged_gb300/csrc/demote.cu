@@ -117,6 +117,47 @@ __global__ void k_debug_read_int2(DevPool P, int seq, int layer, int head, int p
   }
 }
 
+// The inverse: canonical codes and (scale, zero) pairs into the pages. One warp per token; every packed byte holds
+// four codes of one token, so lane l writes one K byte and one V byte.
+__global__ void k_debug_write_int2(DevPool P, int seq, int layer, int head, int pos0, int n, const uint8_t* ck,
+                                   const uint32_t* szk, const uint8_t* cv, const uint32_t* szv) {
+  const int w = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+  if (w >= n) return;
+  const int pos = pos0 + w;
+  const int pg = (pos - kSink) >> 6, tau = (pos - kSink) & (kPage - 1);
+  const int pid = P.page_table[(size_t)seq * P.maxp + pg];
+  if (pid < 0 || pid >= P.max_int2_pages) {
+    if (lane == 0) set_err(P.err, OSCAR_DEVERR_PAGE);
+    return;
+  }
+  uint8_t* blk = P.int2 + (size_t)layer * P.int2_layer_stride + ((size_t)pid * P.Hkv + head) * P.block_bytes;
+  auto gather = [&](const uint8_t* codes, int j0) {  // codes of dims j0, j0 + 8, j0 + 16, j0 + 24 in one byte
+    uint32_t b = 0;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int j = j0 + 8 * p;
+      b |= (uint32_t)((codes[(size_t)w * kCodeBytes + (j >> 2)] >> (2 * (j & 3))) & 3) << (2 * p);
+    }
+    return (uint8_t)b;
+  };
+  {
+    const int tq = lane >> 3, word = (lane >> 2) & 1, e = (lane >> 1) & 1, sh8 = lane & 1;
+    blk[tau * kCodeBytes + tq * 8 + word * 4 + 2 * e + sh8] = gather(ck, word * 64 + sh8 * 32 + tq * 2 + e);
+  }
+  {
+    const int g = lane >> 2, word = lane & 3;
+    const int slice = tau >> 4, ts = tau & 15, tq = (ts >> 1) & 3, e = ts & 1, u = ts >> 3;
+    blk[kPage * kCodeBytes + slice * 512 + (g * 4 + tq) * 16 + 4 * (2 * u + (word >> 1)) + 2 * e + (word & 1)] =
+        gather(cv, word * 32 + g);
+  }
+  const int ng = kHeadDim / P.G;
+  uint32_t* sz = reinterpret_cast<uint32_t*>(blk + 2 * kPage * kCodeBytes);
+  if (lane < ng) {
+    sz[sz_index(tau, lane, ng)] = szk[(size_t)w * ng + lane];
+    sz[kPage * ng + sz_index(tau, lane, ng)] = szv[(size_t)w * ng + lane];
+  }
+}
+
 // Diagnostic: raw INT2 key scores q_rot . k_hat (k_hat = code * s + z per group, fp32) of tokens
 // [pos0, pos0+n) for the hg query heads of one KV head. One warp per token; lane l covers
 // dims 4l..4l+3 of the canonical (rotated, bit-reversed) order.
@@ -238,6 +279,14 @@ cudaError_t launch_debug_read_int2(const DevPool& P, int seq, int layer, int hea
   if (n <= 0) return cudaSuccess;
   k_debug_read_int2<<<(n + 3) / 4, 128, 0, s>>>(P, seq, layer, head, pos0, n, ck, (uint32_t*)szk, cv,
                                                  (uint32_t*)szv);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_debug_write_int2(const DevPool& P, int seq, int layer, int head, int pos0, int n, const uint8_t* ck,
+                                    const void* szk, const uint8_t* cv, const void* szv, cudaStream_t s) {
+  if (n <= 0) return cudaSuccess;
+  k_debug_write_int2<<<(n + 3) / 4, 128, 0, s>>>(P, seq, layer, head, pos0, n, ck, (const uint32_t*)szk, cv,
+                                                 (const uint32_t*)szv);
   return cudaGetLastError();
 }
 

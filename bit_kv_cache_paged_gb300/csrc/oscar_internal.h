@@ -129,6 +129,8 @@ cudaError_t launch_debug_rotate(const DevPool& P, int layer, int head, int kv, c
                                 float* out, cudaStream_t s);
 cudaError_t launch_debug_read_int2(const DevPool& P, int seq, int layer, int head, int pos0, int n,
                                    uint8_t* ck, void* szk, uint8_t* cv, void* szv, cudaStream_t s);
+cudaError_t launch_debug_write_int2(const DevPool& P, int seq, int layer, int head, int pos0, int n, const uint8_t* ck,
+                                    const void* szk, const uint8_t* cv, const void* szv, cudaStream_t s);
 cudaError_t launch_debug_read_bf16(const DevPool& P, int seq, int sink_page, int L, int F,
                                    int layer, int head, int pos0, int n, void* k, void* v,
                                    cudaStream_t s);

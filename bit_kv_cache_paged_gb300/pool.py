@@ -196,6 +196,15 @@ class Pool:
         B.oscar_debug_read_int2(self.handle, seq_id, layer, kv_head, pos0, n, ck, szk, cv, szv, _stream())
         return ck, szk, cv, szv
 
+    def debug_write_int2(self, seq_id, layer, kv_head, pos0, codes_k, sz_k, codes_v, sz_v):
+        """Replace INT2 tokens from pos0 on by canonical codes [n][32] and (scale, zero) [n][groups][2], the
+        layouts of debug_read_int2."""
+        n, ng = codes_k.shape[0], HEAD_DIM // self.group_size
+        for t, dtype, shape, name in ((codes_k, torch.uint8, (n, 32), "codes_k"), (sz_k, torch.float16, (n, ng, 2), "sz_k"),
+                                      (codes_v, torch.uint8, (n, 32), "codes_v"), (sz_v, torch.float16, (n, ng, 2), "sz_v")):
+            _need(t, dtype, shape, name)
+        B.oscar_debug_write_int2(self.handle, seq_id, layer, kv_head, pos0, n, codes_k, sz_k, codes_v, sz_v, _stream())
+
     def debug_int2_scores(self, seq_id, layer, kv_head, q_rot_rows, pos0, n):
         """fp32 [hg][n]: q_rot_rows[h] . k_hat for INT2 tokens [pos0, pos0+n) (no 1/sqrt(d))."""
         hg = self.Hq // self.Hkv

@@ -435,6 +435,14 @@ oscar_status oscar_debug_read_int2(oscar_pool* pool, int32_t seq_id, int32_t lay
                                    int32_t kv_head, int32_t pos0, int32_t n, void* codes_k,
                                    void* sz_k, void* codes_v, void* sz_v, void* stream);
 
+/* The inverse of oscar_debug_read_int2: replace the codes and (scale, zero) pairs of INT2 tokens
+ * [pos0, pos0+n) by the given ones, same layouts (a cache with chosen contents; pages shared with
+ * other sequences change for them too). */
+oscar_status oscar_debug_write_int2(oscar_pool* pool, int32_t seq_id, int32_t layer,
+                                    int32_t kv_head, int32_t pos0, int32_t n, const void* codes_k,
+                                    const void* sz_k, const void* codes_v, const void* sz_v,
+                                    void* stream);
+
 /* Diagnostic scores of INT2 tokens [pos0, pos0+n) of (seq, layer, kv_head): for each of the KV
  * head's hg = Hq/Hkv query heads, q_rot[h] . k_hat(token) in fp32, with k_hat = code*s + z the
  * dequantised rotated key (no 1/sqrt(d) scale). q_rot: dev fp32 [hg][128] (rows of oscar_rotate_q's

@@ -431,6 +431,33 @@ def test_pool_bad_page_is_reported():
     m.pool.check()
 
 
+@pytest.mark.parametrize("group", [128, 32])
+def test_pool_history_with_chosen_contents(group):
+    """Codes, scales and zeros written back as they were read change nothing, and chosen ones are what the chunk sees:
+    zero scales, large ones, all codes alike."""
+    m = Mixed(hq=8, hkv=2, group=group, seed=15)
+    m.add(0)
+    m.chunk([0], [1000])
+    n = m.pool.seq_info(0)[1] - 64
+    g = torch.Generator(device="cuda").manual_seed(16)
+    for h in (0, 1):
+        c = m.pool.debug_read_int2(0, 0, h, 64, n)
+        m.pool.debug_write_int2(0, 0, h, 64, *c)
+        assert all(torch.equal(a, b) for a, b in zip(c, m.pool.debug_read_int2(0, 0, h, 64, n)))
+        for a in (0, 2):
+            c[a][:] = torch.randint(0, 256, c[a].shape, generator=g, device="cuda").byte()
+        c[0][5:70], c[2][300:330] = 255, 0
+        for a in (1, 3):
+            c[a][:] = torch.randn(c[a].shape, generator=g, device="cuda").half()
+            c[a][10:20, :, 0] = 0  # constant rows
+        c[3][40], c[1][50] = 500.0, 0.0
+        m.pool.debug_write_int2(0, 0, h, 64, *c)
+        assert all(torch.equal(a, b) for a, b in zip(c, m.pool.debug_read_int2(0, 0, h, 64, n)))
+    with pytest.raises(B.OscarError):
+        m.pool.debug_write_int2(0, 0, 0, 65, *c)
+    m.chunk([0], [9])
+
+
 def test_pool_chunk_on_a_stream_and_in_graphs():
     m = Mixed(hq=8, hkv=2, seed=14)
     m.add(0)
