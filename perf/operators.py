@@ -248,6 +248,16 @@ def prepare(case, seed):
         pool.step_begin(ids, [int(x) for x in ctx])
         if ctx.sum():
             pool.append_and_demote(0, *(torch.cat([h[i, :int(ctx[i])] for i in ids]).contiguous() for h in hist))
+        # the pool's own demote rounds a few codes and scales in a million the other way: the history given is what counts
+        for i in ids:
+            front = int(st["front"][i])
+            for h in range(hkv) if front > SINK else ():
+                hist_i = []
+                for c, sc, z in (st["kq"], st["vq"]):
+                    c = c[i, SINK:front, h].reshape(front - SINK, 32, 4).int()
+                    hist_i.append((c << (2 * torch.arange(4, device="cuda"))).sum(-1).to(torch.uint8).contiguous())
+                    hist_i.append(torch.stack([sc[i, SINK:front, h, :, 0], z[i, SINK:front, h, :, 0]], -1).contiguous())
+                pool.debug_write_int2(i, 0, h, SINK, *hist_i)
         pool.step_begin(ids, [int(x) for x in new])
         st["pool"] = pool
     return st
