@@ -54,18 +54,10 @@ constexpr uint32_t kIdescBase = (1u << 4) | ((uint32_t)(kTile >> 3) << 17) | ((u
 constexpr uint32_t kIdescBf16 = kIdescBase | (1u << 7) | (1u << 10);  // A, B bf16; fp16 without these bits
 constexpr uint32_t kIdescMn = 1u << 16;                               // B with its N axis contiguous
 
-// Shared-memory descriptors of 128-byte-swizzled tiles: K-major (row r of a 64-dim half at r * 128),
-// and the same bytes read with the other axis contiguous (leading offset: the next 64 of N; stride
-// offset: the next 8 of K).
-__device__ __forceinline__ uint64_t desc_k(uint32_t a) {
-  return (uint64_t)((a >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
-         ((uint64_t)2 << 61);
-}
-__device__ __forceinline__ uint64_t desc_mn(uint32_t a) {
-  return (uint64_t)((a >> 4) & 0x3FFF) | ((uint64_t)(kHalfBytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-__device__ __forceinline__ uint32_t kstep(int k) { return (uint32_t)((k >> 2) * kHalfBytes + (k & 3) * 32); }
+// Lower descriptor words of 128-byte-swizzled tiles: K-major (row r of a 64-dim half at r * 128), and
+// the same bytes read with the other axis contiguous (leading offset: the next 64 of N).
+__device__ __forceinline__ uint32_t desc_k(uint32_t a) { return (a >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t a) { return (a >> 4) | ((uint32_t)(kHalfBytes >> 4) << 16); }
 
 struct ChunkArgs {
   int32_t Hq, Hkv, hg, n_seqs, n_tokens, rows;  // rows: rows of a partial slot
@@ -351,6 +343,7 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared* sh, ui
     int row[2];
     const CUtensorMap* map[2][2];
     bool rows3 = false;
+#pragma unroll
     for (int x = 0; x < 2; ++x) {
       hf[x] = half_of<MIXED>(cur.s, k, x);
       if constexpr (MIXED) {
@@ -381,13 +374,16 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared* sh, ui
       }
     }
     const int n = (hf[0].hi > hf[0].lo) + (hf[1].hi > hf[1].lo);
+#pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       uint8_t* dst;
       uint64_t* bar;
       if (!stage(dst, bar)) return false;
       mbar_expect_tx(bar, n * 2 * kPageHalfBytes);
+#pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (hf[x].hi <= hf[x].lo) continue;
+#pragma unroll
         for (int d = 0; d < 2; ++d) {
           uint8_t* to = dst + d * kHalfBytes + x * kPageHalfBytes;
           if (MIXED && rows3)
@@ -463,7 +459,8 @@ __device__ __forceinline__ void clean_v(uint8_t* tile, uint64_t live0, uint64_t 
 
 template <bool MIXED>
 __device__ void mma_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, uint8_t* ring, Cursor<MIXED> cur, int lane) {
-  const uint32_t tmem = sh->tmem, aq = smem_u32(sq), ar = smem_u32(ring);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem, 0), aq = smem_u32(sq), ar = smem_u32(ring);
+  const uint32_t one = elect_one();
   Ring r;
   uint32_t qn = 0, pn[2] = {0, 0}, seg = 0;
   bool ok = true;
@@ -479,21 +476,14 @@ __device__ void mma_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, uint8_t* r
     tc_fence_after();
     return w;
   };
-  auto addr = [&](uint32_t pos) { return ar + (pos % kStages) * kTileBytes; };
+  auto addr = [&](uint32_t pos) { return ar + (__shfl_sync(0xffffffffu, pos, 0) % kStages) * kTileBytes; };
   auto qk = [&](int u, uint32_t b, uint32_t idesc, bool acc) {
-    if (lane == 0)
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        tc_mma_ss(S(u), desc_k(aq + u * kTileBytes + kstep(k)), desc_k(b + kstep(k)), idesc, acc || k > 0);
+    tc_gemm_ss(S(u), desc_k(aq + u * kTileBytes), desc_k(b), idesc, acc, one);
   };
   auto pv = [&](int u, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
-    if (lane == 0)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) tc_mma_ts(O(u), a + 8 * k, desc_mn(b + k * 2048), idesc | kIdescMn, acc || k > 0);
+    tc_gemm_ts(O(u), a, desc_mn(b), idesc | kIdescMn, acc, one);
   };
-  auto commit = [&](uint64_t* bar) {
-    if (lane == 0) tc_commit(bar);
-  };
+  auto commit = [&](uint64_t* bar) { tc_commit_elected(bar, one); };
 
   for (; ok && cur.valid(); cur.next(C)) {
     if (cur.empty()) continue;
@@ -592,7 +582,11 @@ __device__ void mma_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, uint8_t* r
 }
 
 // ---- softmax warps: one thread per row -----------------------------------------------------------
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 
 template <bool MIXED>
 __device__ void softmax_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, Cursor<MIXED> cur, int u) {
@@ -701,25 +695,28 @@ __device__ void softmax_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, Cursor
         }
       }
       const float nm = m == -INFINITY ? 0.f : -m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      // two scores an instruction, but for the exponentials
+      const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        uint32_t p[32];
+      for (int c = 0; c < 4; ++c) {
+        uint32_t p[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float x = fast_exp2(fmaf(__uint_as_float(s[2 * hh + (i >> 4)][2 * (i & 15)]), scale, nm));
-          const float y = fast_exp2(fmaf(__uint_as_float(s[2 * hh + (i >> 4)][2 * (i & 15) + 1]), scale, nm));
-          sum[i & 3] += x + y;
+        for (int i = 0; i < 16; ++i) {
+          float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), sc2, nm2);
+          x.x = fast_exp2(x.x);
+          x.y = fast_exp2(x.y);
+          sum[i & 1] = __fadd2_rn(sum[i & 1], x);
           if (MIXED && half16) {
-            p[i] = pack_half2(x, y);
+            p[i] = pack_half2(x.x, x.y);
           } else {
-            const __nv_bfloat162 w = __floats2bfloat162_rn(x, y);
+            const __nv_bfloat162 w = __floats2bfloat162_rn(x.x, x.y);
             p[i] = *reinterpret_cast<const uint32_t*>(&w);
           }
         }
-        tc_st32(tS + 32 * hh, p);
+        tc_st16(tS + 16 * c, p);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
       tc_st_wait();
       ready();
       have = true;

@@ -89,20 +89,60 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// D[tmem] (+)= A . B^T, kind::f16: A and B in shared memory, or A in tensor memory (two 16-bit
-// values a column).
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// The upper word of the shared-memory descriptors used here: 128-byte swizzle, descriptor version of
+// the sm_100 family, 1024 bytes from 8 rows to the next 8. The lower word holds the address and the
+// leading offset in 16-byte units.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// One lane of a converged warp (non-zero there).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e;
+}
+
+// D[tmem] (+)= A . B^T of 128 x 128 x 128, kind::f16, as eight steps of 16: A and B tiles in shared
+// memory K-major, their 128 columns two halves of 16 KB (a, b: lower descriptor words); or A in tensor
+// memory (two 16-bit values a column) and B's tile with its N axis contiguous. The whole warp comes
+// here, so that addresses stay in uniform registers, and the elected lane issues: with a branch
+// around each product, issuing one took twice as long as computing it.
+__device__ __forceinline__ void tc_gemm_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate, uint32_t elected) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n .reg .pred p, t, e;\n .reg .b32 x;\n .reg .b64 a, b;\n"
+      " setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, 0, 0;\n setp.ne.b32 e, %6, 0;\n"
+      " add.u32 x, %1, 0;\n mov.b64 a, {x, %4};\n add.u32 x, %2, 0;\n mov.b64 b, {x, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n"
+      " add.u32 x, %1, 2;\n mov.b64 a, {x, %4};\n add.u32 x, %2, 2;\n mov.b64 b, {x, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u32 x, %1, 4;\n mov.b64 a, {x, %4};\n add.u32 x, %2, 4;\n mov.b64 b, {x, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u32 x, %1, 6;\n mov.b64 a, {x, %4};\n add.u32 x, %2, 6;\n mov.b64 b, {x, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u32 x, %1, 1024;\n mov.b64 a, {x, %4};\n add.u32 x, %2, 1024;\n mov.b64 b, {x, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u32 x, %1, 1026;\n mov.b64 a, {x, %4};\n add.u32 x, %2, 1026;\n mov.b64 b, {x, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u32 x, %1, 1028;\n mov.b64 a, {x, %4};\n add.u32 x, %2, 1028;\n mov.b64 b, {x, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u32 x, %1, 1030;\n mov.b64 a, {x, %4};\n add.u32 x, %2, 1030;\n mov.b64 b, {x, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      "}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"((uint32_t)accumulate), "r"(elected)
       : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void tc_gemm_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate, uint32_t elected) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n .reg .pred p, t, e;\n .reg .b32 x, y;\n .reg .b64 b;\n"
+      " setp.ne.b32 p, %5, 0;\n setp.eq.b32 t, 0, 0;\n setp.ne.b32 e, %6, 0;\n"
+      " add.u32 y, %1, 0;\n add.u32 x, %2, 0;\n mov.b64 b, {x, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], b, %3, p;\n"
+      " add.u32 y, %1, 8;\n add.u32 x, %2, 128;\n mov.b64 b, {x, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], b, %3, t;\n"
+      " add.u32 y, %1, 16;\n add.u32 x, %2, 256;\n mov.b64 b, {x, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], b, %3, t;\n"
+      " add.u32 y, %1, 24;\n add.u32 x, %2, 384;\n mov.b64 b, {x, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], b, %3, t;\n"
+      " add.u32 y, %1, 32;\n add.u32 x, %2, 512;\n mov.b64 b, {x, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], b, %3, t;\n"
+      " add.u32 y, %1, 40;\n add.u32 x, %2, 640;\n mov.b64 b, {x, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], b, %3, t;\n"
+      " add.u32 y, %1, 48;\n add.u32 x, %2, 768;\n mov.b64 b, {x, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], b, %3, t;\n"
+      " add.u32 y, %1, 56;\n add.u32 x, %2, 896;\n mov.b64 b, {x, %4};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [y], b, %3, t;\n"
+      "}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"((uint32_t)accumulate), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_elected(uint64_t* bar, uint32_t elected) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(elected)
       : "memory");
 }
 
