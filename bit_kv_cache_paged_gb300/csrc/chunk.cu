@@ -43,12 +43,16 @@ namespace {
 constexpr int kTile = 128;                    // rows of a tile, keys of a block
 constexpr int kHalfBytes = kTile * 128;       // 64 dims of 128 rows
 constexpr int kTileBytes = 2 * kHalfBytes;    // 128 x 128 16-bit values
-constexpr int kStages = 5;                    // K / V tiles in flight
+template <bool MIXED>
+constexpr int kStages = MIXED ? 4 : 5;        // K / V tiles in flight
+constexpr int kCodeBuf = 3 * 2 * int2_block_bytes(128);  // packed INT2 pages in flight: three blocks (two of groups of 32)
+constexpr int kMaxSlots = 3;
 constexpr int kMaxCtas = 152;
 constexpr int kPageHalfBytes = kPage * 128;   // 64 dims of one page
-constexpr float kLazy = 8.f;                  // the maximum may lag by 2^8 before O is rescaled
+constexpr float kGrown = 16384.f;             // a block's weights under an old maximum: fp16 holds each of them
 constexpr int kDescBytes = 32;
-constexpr int kMinUnits = 2;                  // key blocks per CTA, at least, before a call is cut further
+constexpr int kItemUnits = 2;                 // what an item costs besides its blocks (queries in, output out, pipeline)
+constexpr int kMinUnits = 4;                  // units per CTA, at least, before a call is cut further
 
 constexpr uint32_t kIdescBase = (1u << 4) | ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
 constexpr uint32_t kIdescBf16 = kIdescBase | (1u << 7) | (1u << 10);  // A, B bf16; fp16 without these bits
@@ -60,7 +64,8 @@ __device__ __forceinline__ uint32_t desc_k(uint32_t a) { return (a >> 4) | (1u <
 __device__ __forceinline__ uint32_t desc_mn(uint32_t a) { return (a >> 4) | ((uint32_t)(kHalfBytes >> 4) << 16); }
 
 struct ChunkArgs {
-  int32_t Hq, Hkv, hg, n_seqs, n_tokens, rows;  // rows: rows of a partial slot
+  int32_t Hq, Hkv, hg, lg, n_seqs, n_tokens, rows;  // lg: log2 of a tile pair's tokens; rows: of a partial slot
+  int32_t wide;                                 // out starts on a 32-byte boundary
   // BF16-only cache
   const int32_t *page_table, *lengths, *cu;
   const uint8_t* v_pages;
@@ -125,59 +130,60 @@ __device__ __forceinline__ SeqWork load_seq(const ChunkArgs& C, int i) {
   return s;
 }
 
-// Key blocks that tile pair t of a sequence really has, and the units it counts for (at least one).
-__device__ __forceinline__ int real_blocks(const SeqWork& s, int bt, int t) {
-  const int keys = s.A + min(s.n, bt * (t + 1));
+// Key blocks that tile pair t of a sequence really has.
+__device__ __forceinline__ int real_blocks(const SeqWork& s, int lg, int t) {
+  const int keys = s.A + min(s.n, (t + 1) << lg);
   return s.nI + s.nB + (keys > 0 ? (keys + kTile - 1) / kTile : 0);
 }
 
-// Units of the tile pairs 0 .. t-1, all of them full (bt tokens, a power of two up to 256):
-// sum over u < t of max(1, pre + ceil((A + bt (u + 1)) / 128)).
-__device__ __forceinline__ int64_t units_before(const SeqWork& s, int bt, int64_t t) {
-  const int64_t n0 = s.A < 0 ? min((int64_t)(-s.A / bt), t) : 0;  // pairs without a key
-  const int64_t m = t - n0, c = s.A + bt * n0 + bt + kTile - 1, q = c >> 7;
-  int64_t sum = n0 + m * (s.nI + s.nB + q);
-  if (bt >= kTile) return sum + (bt / kTile) * (m * (m - 1) / 2);
-  const int r = kTile / bt, d = (int)(c & 127), w0 = (kTile - d + bt - 1) / bt;  // remainders >= w0 carry
-  const int64_t M = m / r, rem = m - M * r;
-  return sum + r * (M * (M - 1) / 2) + M * (r - w0) + rem * M + max((int64_t)0, rem - w0);
+// Units of the tile pairs 0 .. t-1, all of them full (2^lg tokens, 16 to 256):
+// sum over u < t of max(1, pre + ceil((A + 2^lg (u + 1)) / 128)) + kItemUnits.
+__device__ __forceinline__ int64_t units_before(const SeqWork& s, int lg, int t) {
+  const int bt = 1 << lg;
+  const int n0 = s.A < 0 ? min(-s.A >> lg, t) : 0;  // pairs without a key
+  const int m = t - n0, c = s.A + (n0 << lg) + bt + kTile - 1;
+  const int64_t sum = (int64_t)n0 + (int64_t)t * kItemUnits + (int64_t)m * (s.nI + s.nB + (c >> 7));
+  if (bt >= kTile) return sum + (int64_t)(bt >> 7) * (((int64_t)m * (m - 1)) >> 1);
+  const int lr = 7 - lg, r = 1 << lr, w0 = (kTile - (c & 127) + bt - 1) >> lg;  // remainders >= w0 carry
+  const int64_t M = m >> lr;
+  const int rem = m & (r - 1);
+  return sum + r * ((M * (M - 1)) >> 1) + M * (r - w0) + rem * M + max(0, rem - w0);
 }
-__device__ __forceinline__ int pairs_of(const SeqWork& s, int bt) { return (s.n + bt - 1) / bt; }
-__device__ __forceinline__ int64_t units_of(const SeqWork& s, int bt) {  // of one KV head
-  const int T = pairs_of(s, bt);
-  return T ? units_before(s, bt, T - 1) + max(1, real_blocks(s, bt, T - 1)) : 0;
+__device__ __forceinline__ int pairs_of(const SeqWork& s, int lg) { return (s.n + (1 << lg) - 1) >> lg; }
+__device__ __forceinline__ int64_t units_of(const SeqWork& s, int lg) {  // of one KV head
+  const int T = pairs_of(s, lg);
+  return T ? units_before(s, lg, T - 1) + max(1, real_blocks(s, lg, T - 1)) + kItemUnits : 0;
 }
+// The block in front of which a boundary x units behind an item's start cuts it.
+__device__ __forceinline__ int cut_at(int64_t x, int nb) { return (int)min((int64_t)nb, max((int64_t)0, x - kItemUnits / 2)); }
 
-// A place in the order (sequence, KV head, tile pair, block), moved segment by segment.
+// A place in the order (sequence, KV head, tile pair, block), moved segment by segment up to the
+// CTA's end.
 template <bool MIXED>
 struct Cursor {
   SeqWork s;
   int i, h, t, k0, k1, nb;  // the segment: blocks [k0, k1) of nb
-  int64_t left;             // units from k0 on
-  int bt;
+  int lg;
+  int64_t end;              // units from the item's start to the CTA's end
 
-  __device__ __forceinline__ void start(const ChunkArgs& C, int i_, int h_, int t_, int k, int64_t n) {
-    bt = 2 * kTile / C.hg;
+  __device__ __forceinline__ void start(const ChunkArgs& C, int i_, int h_, int t_, int64_t x, int64_t n) {
+    lg = C.lg;
     i = i_;
     h = h_;
     t = t_;
-    k0 = k;
-    left = n;
-    if (left > 0) {
-      s = load_seq<MIXED>(C, i);
-      fit();
-    }
+    end = x + n;
+    s = load_seq<MIXED>(C, i);
+    nb = max(1, real_blocks(s, lg, t));
+    k0 = cut_at(x, nb);
+    k1 = cut_at(end, nb);
+    if (k0 >= nb) next(C);
   }
-  __device__ __forceinline__ void fit() {
-    nb = max(1, real_blocks(s, bt, t));
-    k1 = (int)min((int64_t)nb, k0 + left);
-  }
-  __device__ __forceinline__ bool valid() const { return left > 0; }
+  __device__ __forceinline__ bool valid() const { return k1 > k0; }
   __device__ __forceinline__ void next(const ChunkArgs& C) {
-    left -= k1 - k0;
-    if (left <= 0) return;
-    k0 = 0;
-    if (++t >= pairs_of(s, bt)) {
+    end -= nb + kItemUnits;
+    k0 = k1 = 0;
+    if (end <= kItemUnits / 2) return;
+    if (++t >= pairs_of(s, lg)) {
       t = 0;
       if (++h >= C.Hkv) {
         h = 0;
@@ -187,11 +193,15 @@ struct Cursor {
         } while (s.n == 0 && i + 1 < C.n_seqs);
       }
     }
-    fit();
+    nb = max(1, real_blocks(s, lg, t));
+    k1 = cut_at(end, nb);
   }
-  __device__ __forceinline__ bool empty() const { return real_blocks(s, bt, t) == 0; }
-  __device__ __forceinline__ int tokens() const { return min(bt, s.n - t * bt); }
-  __device__ __forceinline__ bool two() const { return tokens() > bt / 2; }  // the second tile has rows
+  __device__ __forceinline__ bool empty() const { return real_blocks(s, lg, t) == 0; }
+  __device__ __forceinline__ int tokens() const { return min(1 << lg, s.n - (t << lg)); }
+  __device__ __forceinline__ bool two() const { return tokens() > (1 << lg) / 2; }  // the second tile has rows
+  // Causal keys that every row of the pair sees, and that any does.
+  __device__ __forceinline__ int keys_all() const { return max(s.A + (t << lg) + 1, 0); }
+  __device__ __forceinline__ int keys_any() const { return s.A + min(s.n, (t + 1) << lg); }
 };
 
 // Where one half block of 64 keys comes from, and its slots [lo, hi) that hold keys for anyone.
@@ -232,27 +242,50 @@ __device__ __forceinline__ uint64_t bits(int lo, int hi) {  // bits [lo, hi) of 
 }
 
 // ------------------------------------------------------------------------------------------------
+// A V tile to be cleaned: rows outside live are zeroed, rows [lo, hi) searched for non-finite values.
+struct Clean {
+  uint64_t live0, live1;
+  int32_t stage, lo, hi, slot;  // slot: row of `bad` that takes the keys found; stage -1: no more
+};
+
+template <bool MIXED>
 struct Shared {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t q_full, q_empty, s_full[2], p_ready[2], done;
+  uint64_t full[kStages<MIXED>], empty[kStages<MIXED>], code_full[kMaxSlots], code_empty[kMaxSlots];
+  uint64_t q_full, q_empty, s_full[2], p_ready[2], done, clean_go, clean_done;
   uint32_t tmem;
   int32_t abort;
   // plan
-  int64_t total, scan[16];
-  int32_t st_i, st_h, st_t, st_k;
+  int64_t total, st_x, scan[16];
+  int32_t st_i, st_h, st_t;
+  Clean clean;
   // non-finite values of the diagonal blocks: key bits per block, two segments in turn
   uint32_t bad[2][4][4];
   uint32_t any_bad[2];
+  Cursor<MIXED> cursors[8];  // of the softmax warps, whose registers hold scores
 };
-static_assert(sizeof(Shared) <= 1024, "Shared");
-constexpr int kChunkSmem = 2 * kTileBytes + kStages * kTileBytes + 1024 + 1024;
+constexpr int kSharedBytes = 2048;
+static_assert(sizeof(Shared<true>) <= kSharedBytes && sizeof(Shared<false>) <= kSharedBytes, "Shared");
+template <bool MIXED>
+constexpr int kChunkSmem = (2 + kStages<MIXED>) * kTileBytes + (MIXED ? kCodeBuf : 0) + kSharedBytes + 1024;
+static_assert(kChunkSmem<true> <= 232448 && kChunkSmem<false> <= 232448, "shared memory of an SM");
 
-// Bounded wait that also ends when another role gave up.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Shared* sh, uint32_t* err) {
+// One try that sleeps up to ns nanoseconds: a spinning warp takes issue slots from the others.
+__device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait that also ends when another role gave up. SLEEP: for roles with time to spare.
+template <bool SLEEP = false, bool MIXED>
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Shared<MIXED>* sh, uint32_t* err) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (SLEEP ? mbar_try_wait_for(bar, parity, 2000) : mbar_try_wait(bar, parity)) return true;
     if (*reinterpret_cast<volatile int32_t*>(&sh->abort)) return false;
     if (clock64() - t0 >= kWaitCycles) break;
   }
@@ -262,57 +295,57 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Shared*
 }
 // The same for a whole warp, which leaves it converged (tensor-memory instructions and aligned
 // barriers follow).
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Shared* sh, uint32_t* err) {
-  const bool ok = wait_bar(bar, parity, sh, err);
+template <bool SLEEP = false, bool MIXED>
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Shared<MIXED>* sh, uint32_t* err) {
+  const bool ok = wait_bar<SLEEP>(bar, parity, sh, err);
   __syncwarp();
   return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// AND over the four warps of the dequantising group (named barrier 1).
-__device__ __forceinline__ bool and128(bool v) {
-  uint32_t out;
-  __syncwarp();
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(out)
-      : "r"((uint32_t)v)
-      : "memory");
-  return out != 0;
-}
-
+template <bool MIXED>
 struct Ring {  // position in the stream of K / V tiles
   uint32_t pos = 0;
-  __device__ __forceinline__ int stage() const { return pos % kStages; }
-  __device__ __forceinline__ uint32_t parity() const { return (pos / kStages) & 1; }
+  __device__ __forceinline__ int stage() const { return pos % kStages<MIXED>; }
+  __device__ __forceinline__ uint32_t parity() const { return (pos / kStages<MIXED>) & 1; }
 };
+// A tile's full barrier counts the four dequantising warps; a tensor copy's lane arrives for all.
+template <bool MIXED>
+__device__ __forceinline__ void expect_tile(uint64_t* bar, uint32_t bytes) {
+  mbar_expect_tx(bar, bytes);
+  if (MIXED)
+    for (int i = 0; i < 3; ++i) mbar_arrive(bar);
+}
+// Blocks of packed pages that fit the code buffer.
+__device__ __forceinline__ int code_slots(const DevPool& P) { return P.ngroups == 1 ? 3 : 2; }
 
 // The two limb tiles of a rotation matrix.
 constexpr int kLimbs = 2;
 
 // ---- tensor-copy warp --------------------------------------------------------------------------
 template <bool MIXED>
-__device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared* sh, uint8_t* sq, uint8_t* ring, Cursor<MIXED> cur) {
+__device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MIXED>* sh, uint8_t* sq, uint8_t* ring, uint8_t* codes,
+                          Cursor<MIXED> cur) {
   // one lane
   const uint64_t keep = policy_evict_last(), once = policy_evict_first();
-  Ring r;
+  Ring<MIXED> r;
   uint32_t issued = 0, qn = 0;  // bit s: stage s has had a tensor copy
   uint32_t last_parity = 0;
   bool ok = true;
   auto load_q = [&]() {
-    if (qn && !wait_bar(&sh->q_empty, (qn - 1) & 1, sh, C.err)) return false;
-    const int tiles = cur.two() ? 2 : 1, tok = cur.s.row0 + cur.t * cur.bt;
+    if (qn && !wait_bar<true>(&sh->q_empty, (qn - 1) & 1, sh, C.err)) return false;
+    const int tiles = cur.two() ? 2 : 1, tok = cur.s.row0 + (cur.t << C.lg);
     mbar_expect_tx(&sh->q_full, tiles * kTileBytes);
     for (int u = 0; u < tiles; ++u)
       for (int d = 0; d < 2; ++d)
-        tma_load_3d(sq + u * kTileBytes + d * kHalfBytes, &M.q, d * 64, cur.h * C.hg, tok + u * (cur.bt / 2), &sh->q_full, once);
+        tma_load_3d(sq + u * kTileBytes + d * kHalfBytes, &M.q, d * 64, cur.h * C.hg, tok + u * ((1 << C.lg) / 2), &sh->q_full, once);
     ++qn;
     return true;
   };
   auto stage = [&](uint8_t*& dst, uint64_t*& bar) {
     const int s = r.stage();
-    if (!wait_bar(&sh->empty[s], r.parity() ^ 1, sh, C.err)) return false;
+    if (!wait_bar<true>(&sh->empty[s], r.parity() ^ 1, sh, C.err)) return false;
     dst = ring + s * kTileBytes;
     bar = &sh->full[s];
     issued |= 1u << s;
@@ -324,7 +357,7 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared* sh, ui
   // tells the phase of a barrier only to a role that has seen every phase of it.
   auto skip = [&](int n) {
     for (; n > 0; --n, ++r.pos)
-      if (!wait_bar(&sh->empty[r.stage()], r.parity() ^ 1, sh, C.err)) return false;
+      if (!wait_bar<true>(&sh->empty[r.stage()], r.parity() ^ 1, sh, C.err)) return false;
     return true;
   };
   auto load_limbs = [&](int kv) {
@@ -333,9 +366,33 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared* sh, ui
       uint8_t* dst;
       uint64_t* bar;
       if (!stage(dst, bar)) return false;
-      mbar_expect_tx(bar, kTileBytes);
+      expect_tile<MIXED>(bar, kTileBytes);
       bulk_g2s(dst, src + l * kTileBytes, kTileBytes, bar, keep);
     }
+    return true;
+  };
+  // The packed pages of INT2 block k, as they lie.
+  uint32_t cpos = 0;
+  auto load_codes = [&](int k) {
+    const int slots = code_slots(C.P), slot = cpos % slots;
+    const int64_t j = 2 * (int64_t)k;
+    const bool second = (j + 1) * kPage < cur.s.hist;
+    const int32_t* pt = C.P.page_table + (size_t)cur.s.seq * C.P.maxp + j;
+    int64_t pid[2] = {pt[0], second ? pt[1] : 0};
+    if (!wait_bar<true>(&sh->code_empty[slot], ((cpos / slots) & 1) ^ 1, sh, C.err)) return false;
+    mbar_expect_tx(&sh->code_full[slot], (second ? 2 : 1) * C.P.block_bytes);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if (x && !second) break;
+      if (pid[x] < 0 || pid[x] >= C.P.max_int2_pages) {
+        set_err(C.err, OSCAR_DEVERR_PAGE);
+        pid[x] = 0;
+      }
+      bulk_g2s(codes + (size_t)(slot * 2 + x) * C.P.block_bytes,
+               C.P.int2 + (size_t)C.layer * C.P.int2_layer_stride + ((size_t)pid[x] * C.Hkv + cur.h) * C.P.block_bytes,
+               C.P.block_bytes, &sh->code_full[slot], keep);
+    }
+    ++cpos;
     return true;
   };
   auto load_block = [&](int k) {
@@ -379,7 +436,7 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared* sh, ui
       uint8_t* dst;
       uint64_t* bar;
       if (!stage(dst, bar)) return false;
-      mbar_expect_tx(bar, n * 2 * kPageHalfBytes);
+      expect_tile<MIXED>(bar, n * 2 * kPageHalfBytes);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (hf[x].hi <= hf[x].lo) continue;
@@ -399,7 +456,9 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared* sh, ui
     if (cur.empty()) continue;
     const int nI = MIXED ? min(cur.k1, cur.s.nI) : 0;
     if (cur.k0 < nI) {
-      ok = load_q() && load_limbs(0) && skip(2 * (nI - cur.k0)) && (C.P.absorbed || load_limbs(1));
+      ok = load_q() && load_limbs(0);
+      for (int k = cur.k0; ok && k < nI; ++k) ok = load_codes(k) && (k < cur.k0 + 2 || skip(2));  // packed pages run ahead
+      ok = ok && skip(2 * min(2, nI - cur.k0)) && (C.P.absorbed || load_limbs(1));
     }
     const int kb = max(cur.k0, nI);
     if (ok && kb < cur.k1) {
@@ -408,66 +467,75 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared* sh, ui
     }
   }
   if (!ok) {  // never leave with a copy in flight
-    for (int s = 0; s < kStages; ++s)
+    for (int s = 0; s < kStages<MIXED>; ++s)
       if ((issued >> s) & 1) mbar_wait(&sh->full[s], (last_parity >> s) & 1, C.err);
     if (qn) mbar_wait(&sh->q_full, (qn - 1) & 1, C.err);
+    if constexpr (MIXED) {
+      const uint32_t slots = code_slots(C.P);
+      for (uint32_t c = cpos > slots ? cpos - slots : 0; c < cpos; ++c) mbar_wait(&sh->code_full[c % slots], (c / slots) & 1, C.err);
+    }
+  }
+}
+
+// ---- cleaning warps (two): a V tile at a time, 64 rows each, while the tile's scores become P ------
+template <bool MIXED>
+__device__ void clean_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* ring, int part, int lane) {
+  for (uint32_t n = 0;; ++n) {
+    if (!wait_warp<true>(&sh->clean_go, n & 1, sh, C.err)) return;
+    const Clean w = sh->clean;
+    if (w.stage < 0) return;
+    const uint64_t live = part ? w.live1 : w.live0;
+    const int lo = min(max(w.lo - 64 * part, 0), 64), hi = min(max(w.hi - 64 * part, 0), 64);
+    // a lane takes one 16-byte chunk of every other row
+    const int c = lane & 15;
+    uint8_t* base = ring + w.stage * kTileBytes + (c >> 3) * kHalfBytes + part * kPageHalfBytes + (c & 7) * 16;
+    if (live != ~0ull)
+      for (int row = lane >> 4; row < 64; row += 2)
+        if (!((live >> row) & 1)) *reinterpret_cast<uint4*>(base + row * 128) = make_uint4(0, 0, 0, 0);
+    uint32_t bad0 = 0, bad1 = 0;
+#pragma unroll 8
+    for (int row = lo + (lane >> 4); row < hi; row += 2) {
+      uint4* p = reinterpret_cast<uint4*>(base + row * 128);
+      uint4 v = *p;
+      uint32_t e[4] = {v.x, v.y, v.z, v.w};
+      uint32_t keep[4], any = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        keep[i] = ((e[i] & 0x7F80u) == 0x7F80u ? 0u : 0xFFFFu) | ((e[i] & 0x7F800000u) == 0x7F800000u ? 0u : 0xFFFF0000u);
+        any |= ~keep[i];
+      }
+      if (any) {
+        *p = make_uint4(e[0] & keep[0], e[1] & keep[1], e[2] & keep[2], e[3] & keep[3]);
+        bad0 |= row < 32 ? 1u << row : 0;
+        bad1 |= row < 32 ? 0 : 1u << (row - 32);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t b = __reduce_or_sync(0xffffffffu, i ? bad1 : bad0);
+      if (b && lane == 0) {
+        sh->bad[w.slot >> 2][w.slot & 3][2 * part + i] = b;
+        sh->any_bad[w.slot >> 2] = 1;
+      }
+    }
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->clean_done);
   }
 }
 
 // ---- tensor-core warp --------------------------------------------------------------------------
-// Zero the rows of a V tile that nobody may see, and on the diagonal the non-finite values of the
-// others, whose keys are returned as bits (per lane group, OR-ed by the caller).
-__device__ __forceinline__ void clean_v(uint8_t* tile, uint64_t live0, uint64_t live1, bool diagonal, uint32_t (&bad)[4], int lane) {
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const uint32_t live = (uint32_t)((w & 2 ? live1 : live0) >> (32 * (w & 1)));
-    uint32_t b = 0;
-    if (live != 0xFFFFFFFFu || diagonal) {
-#pragma unroll 4
-      for (int it = 0; it < 16; ++it) {  // 32 rows x 16 chunks: a lane takes one chunk of 4 rows apart
-        const int row = it * 2 + (lane >> 4), c = lane & 15;
-        uint4* p = reinterpret_cast<uint4*>(tile + (c >> 3) * kHalfBytes + (w * 32 + row) * 128 + (c & 7) * 16);
-        if (!((live >> row) & 1)) {
-          *p = make_uint4(0, 0, 0, 0);
-        } else if (diagonal) {
-          uint4 v = *p;
-          uint32_t* e = reinterpret_cast<uint32_t*>(&v);
-          bool hit = false;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if ((e[i] & 0x7F80u) == 0x7F80u) {
-              e[i] &= 0xFFFF0000u;
-              hit = true;
-            }
-            if ((e[i] & 0x7F800000u) == 0x7F800000u) {
-              e[i] &= 0xFFFFu;
-              hit = true;
-            }
-          }
-          if (hit) {
-            *p = v;
-            b |= 1u << row;
-          }
-        }
-      }
-    }
-    bad[w] = __reduce_or_sync(0xffffffffu, b);
-  }
-  fence_proxy_async();
-  __syncwarp();
-}
-
 template <bool MIXED>
-__device__ void mma_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, uint8_t* ring, Cursor<MIXED> cur, int lane) {
+__device__ void mma_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq, uint8_t* ring, Cursor<MIXED> cur, int lane) {
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem, 0), aq = smem_u32(sq), ar = smem_u32(ring);
   const uint32_t one = elect_one();
-  Ring r;
-  uint32_t qn = 0, pn[2] = {0, 0}, seg = 0;
+  Ring<MIXED> r;
+  uint32_t qn = 0, pn[2] = {0, 0}, seg = 0, cn = 0;
   bool ok = true;
   auto S = [&](int u) { return tmem + (uint32_t)(u * kTile); };
   auto O = [&](int u) { return tmem + (uint32_t)(2 * kTile + u * kTile); };
   auto wait_full = [&](uint32_t pos) {
-    const bool w = wait_warp(&sh->full[pos % kStages], (pos / kStages) & 1, sh, C.err);
+    const bool w = wait_warp(&sh->full[pos % kStages<MIXED>], (pos / kStages<MIXED>) & 1, sh, C.err);
     tc_fence_after();
     return w;
   };
@@ -476,7 +544,7 @@ __device__ void mma_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, uint8_t* r
     tc_fence_after();
     return w;
   };
-  auto addr = [&](uint32_t pos) { return ar + (__shfl_sync(0xffffffffu, pos, 0) % kStages) * kTileBytes; };
+  auto addr = [&](uint32_t pos) { return ar + (__shfl_sync(0xffffffffu, pos, 0) % kStages<MIXED>) * kTileBytes; };
   auto qk = [&](int u, uint32_t b, uint32_t idesc, bool acc) {
     tc_gemm_ss(S(u), desc_k(aq + u * kTileBytes), desc_k(b), idesc, acc, one);
   };
@@ -503,30 +571,36 @@ __device__ void mma_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, uint8_t* r
         qk(u, addr(kpos), idesc, false);
         commit(&sh->s_full[u]);
       }
-      commit(&sh->empty[kpos % kStages]);
+      commit(&sh->empty[kpos % kStages<MIXED>]);
       if (a + 1 == b) commit(&sh->q_empty);
       for (int k = a; k < b; ++k) {
         const uint32_t vpos = kpos + 1;
         if (!wait_full(vpos)) return false;
+        bool dirty = false;
         if (idesc == kIdescBf16) {
-          // causal blocks are those behind the cached ones; the diagonal starts where the pair's first
-          // row ends
-          const int j = k - cur.s.nI - cur.s.nB, j0 = max(cur.s.A + cur.t * cur.bt + 1, 0) / kTile;
-          const bool diagonal = j >= j0;
-          const Half h0 = half_of<MIXED>(cur.s, k, 0), h1 = half_of<MIXED>(cur.s, k, 1);
-          const uint64_t l0 = bits(h0.lo, h0.hi), l1 = bits(h1.lo, h1.hi);
-          if (diagonal || (l0 & l1) != ~0ull) {
-            uint32_t bad[4];
-            clean_v(ring + (vpos % kStages) * kTileBytes, l0, l1, diagonal, bad, lane);
-            if (diagonal && (bad[0] | bad[1] | bad[2] | bad[3])) {
-              if (lane < 4) sh->bad[sb][j - j0][lane] = bad[lane];
-              if (lane == 0) sh->any_bad[sb] = 1;
-              __syncwarp();
-            }
+          uint64_t l0, l1;
+          int lo = kTile, hi = kTile, slot = 0;
+          if (MIXED && k < cur.s.nI + cur.s.nB) {
+            const Half h0 = half_of<MIXED>(cur.s, k, 0), h1 = half_of<MIXED>(cur.s, k, 1);
+            l0 = bits(h0.lo, h0.hi);
+            l1 = bits(h1.lo, h1.hi);
+          } else {  // the diagonal: some rows of the pair see a key and others do not
+            const int j = k - cur.s.nI - cur.s.nB;
+            lo = min(max(cur.keys_all() - j * kTile, 0), kTile);
+            hi = min(cur.keys_any() - j * kTile, kTile);
+            l0 = bits(0, min(hi, 64));
+            l1 = bits(0, max(hi - 64, 0));
+            slot = 4 * sb + j - cur.keys_all() / kTile;
+          }
+          dirty = (l0 & l1) != ~0ull || lo < hi;
+          if (dirty && lane == 0) {
+            sh->clean = {l0, l1, (int)(vpos % kStages<MIXED>), lo, hi, slot};
+            mbar_arrive(&sh->clean_go);
           }
         }
         for (int u = 0; u < tiles; ++u) {
           if (!wait_p(u)) return false;
+          if (u == 0 && dirty && !wait_warp(&sh->clean_done, cn++ & 1, sh, C.err)) return false;
           pv(u, S(u), addr(vpos), idesc, acc);
           if (k + 1 < b) {
             if (u == 0 && !wait_full(vpos + 1)) return false;
@@ -535,9 +609,9 @@ __device__ void mma_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, uint8_t* r
           commit(&sh->s_full[u]);  // the next S, or behind the last block O
         }
         acc = true;
-        commit(&sh->empty[vpos % kStages]);
+        commit(&sh->empty[vpos % kStages<MIXED>]);
         kpos = vpos + 1;
-        if (k + 1 < b) commit(&sh->empty[kpos % kStages]);
+        if (k + 1 < b) commit(&sh->empty[kpos % kStages<MIXED>]);
         if (k + 2 == b) commit(&sh->q_empty);
       }
       r.pos = kpos;
@@ -551,8 +625,8 @@ __device__ void mma_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, uint8_t* r
         qk(u, addr(r.pos + 1), kIdescBf16, true);
         commit(&sh->s_full[u]);
       }
-      commit(&sh->empty[r.pos % kStages]);
-      commit(&sh->empty[(r.pos + 1) % kStages]);
+      commit(&sh->empty[r.pos % kStages<MIXED>]);
+      commit(&sh->empty[(r.pos + 1) % kStages<MIXED>]);
       r.pos += kLimbs;
       for (int u = 0; ok && u < tiles; ++u) ok = wait_p(u);  // Q R_K is in shared memory
       ok = ok && blocks(cur.k0, nI, kIdescBase);
@@ -567,14 +641,18 @@ __device__ void mma_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, uint8_t* r
           pv(u, S(u) + 64, addr(r.pos), kIdescBf16, true);
           if (nI == cur.k1) commit(&sh->s_full[u]);
         }
-        commit(&sh->empty[r.pos % kStages]);
-        commit(&sh->empty[(r.pos + 1) % kStages]);
+        commit(&sh->empty[r.pos % kStages<MIXED>]);
+        commit(&sh->empty[(r.pos + 1) % kStages<MIXED>]);
         r.pos += kLimbs;
       }
     }
     const int kb = max(cur.k0, nI);
     if (ok && kb < cur.k1) ok = wait_warp(&sh->q_full, qn++ & 1, sh, C.err) && blocks(kb, cur.k1, kIdescBf16);
     if (ok && tiles == 1) ok = wait_p(1);
+  }
+  if (lane == 0) {
+    sh->clean.stage = -1;
+    mbar_arrive(&sh->clean_go);
   }
   // no product in flight when the tensor memory is given back
   commit(&sh->done);
@@ -588,14 +666,35 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// 32 bytes of a thread's own row, one sector: in one store where the row starts on such a boundary.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                 "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 template <bool MIXED>
-__device__ void softmax_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, Cursor<MIXED> cur, int u) {
+__device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq, const Cursor<MIXED>& start, int u) {
   const int row = threadIdx.x & 127, warp = row >> 5;
   const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
   const uint32_t tS = sh->tmem + lane_off + u * kTile, tO = sh->tmem + lane_off + 2 * kTile + u * kTile;
   uint32_t sn = 0, seg = 0;
   bool ok = true;
   const int hg = C.hg, tpt = kTile / hg;
+  // this warp's cursor, moved by its first lane
+  Cursor<MIXED>& cur = sh->cursors[threadIdx.x >> 5];
+  if ((threadIdx.x & 31) == 0) cur = start;
+  __syncwarp();
+  auto next = [&]() {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) cur.next(C);
+    __syncwarp();
+  };
   auto wait_s = [&]() {
     const bool w = wait_warp(&sh->s_full[u], sn++ & 1, sh, C.err);
     tc_fence_after();
@@ -605,16 +704,9 @@ __device__ void softmax_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, Cursor
     tc_fence_before();
     mbar_arrive(&sh->p_ready[u]);
   };
-  auto load_s = [&](uint32_t (&s)[4][32]) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tc_ld32_issue(tS + 32 * c, s[c]);
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tc_ld_wait_pass(s[c]);
-  };
 
-  for (; ok && cur.valid(); cur.next(C)) {
-    const int tok = cur.t * cur.bt + u * tpt + row / hg;  // this row's token of the sequence
+  for (; ok && cur.valid(); next()) {
+    const int tok = (cur.t << C.lg) + u * tpt + row / hg;  // this row's token of the sequence
     const bool live = tok < cur.s.n;
     const bool whole = cur.k0 == 0 && cur.k1 == cur.nb;
     const int head = cur.h * hg + row % hg;
@@ -639,9 +731,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, Cursor
 
     auto block = [&](int k, float scale, bool half16) {
       if (!wait_s()) return false;
-      uint32_t s[4][32];
-      load_s(s);
-      // the columns this row may see
+      // scores of columns this row may not see
       uint64_t b0 = ~0ull, b1 = ~0ull;
       bool masked;
       if (MIXED && k < cur.s.nI + cur.s.nB) {
@@ -658,65 +748,86 @@ __device__ void softmax_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, Cursor
         }
       }
       if (masked) {
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
+          uint32_t x[32];
+          tc_ld32_issue(tS + 32 * c, x);
+          tc_ld_wait1(x);
           const uint32_t b = (uint32_t)((c & 2 ? b1 : b0) >> (32 * (c & 1)));
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (!((b >> i) & 1)) s[c][i] = 0xFF800000u;
+            if (!((b >> i) & 1)) x[i] = 0xFF800000u;
+          tc_st32(tS + 32 * c, x);
         }
+        tc_st_wait();
       }
-      float mx[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        mx[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-        for (int i = 1; i < 31; i += 2) mx[c] = max3(mx[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
-        mx[c] = fmaxf(mx[c], __uint_as_float(s[c][31]));
-      }
-      const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-      // the maximum moves only when it would grow by more than 2^kLazy; sums stay far inside fp32
-      const bool move = mb > m + kLazy || (m == -INFINITY && mb > m);
-      if (__any_sync(0xffffffffu, move)) {
-        const float mn = move ? mb : m, alpha = move ? fast_exp2(m - mn) : 1.f;
-        m = mn;
-        l *= alpha;
-        if (have) {
+      // The maximum is taken anew only where it must be: for the rows' first block, and when the weights
+      // under the last one sum to more than kGrown (they are finite then, or their sum is infinite), in
+      // which case they are made again.
+      uint32_t p[4][16];
+      float2 sum[2];
+      for (bool fresh = __any_sync(0xffffffffu, m == -INFINITY);; fresh = true) {
+        if (fresh) {
+          float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tc_ld32_issue(tO + 32 * c, o);
-            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-            tc_ld_wait_pass(o);
+            uint32_t x[32];
+            tc_ld32_issue(tS + 32 * c, x);
+            tc_ld_wait1(x);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tc_st32(tO + 32 * c, o);
+            for (int i = 0; i < 32; i += 4) {
+              mx0 = max3(mx0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+              mx1 = max3(mx1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+            }
+          }
+          const float mb = fmaxf(mx0, mx1) * scale;
+          const float mn = fmaxf(m, mb), alpha = mb > m ? fast_exp2(m - mn) : 1.f;
+          m = mn;
+          l *= alpha;
+          if (have) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tc_ld32_issue(tO + 32 * c, o);
+              tc_ld_wait1(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tc_st32(tO + 32 * c, o);
+            }
           }
         }
-      }
-      const float nm = m == -INFINITY ? 0.f : -m;
-      // two scores an instruction, but for the exponentials
-      const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // two scores an instruction, but for the exponentials
+        const float nm = m == -INFINITY ? 0.f : -m;
+        const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
+        sum[0] = sum[1] = make_float2(0.f, 0.f);
+        uint32_t x[2][32];
+        tc_ld32_issue(tS, x[0]);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t p[16];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t(&y)[32] = x[c & 1];
+          tc_ld_wait1(y);
+          if (c < 3) tc_ld32_issue(tS + 32 * (c + 1), x[(c + 1) & 1]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), sc2, nm2);
-          x.x = fast_exp2(x.x);
-          x.y = fast_exp2(x.y);
-          sum[i & 1] = __fadd2_rn(sum[i & 1], x);
-          if (MIXED && half16) {
-            p[i] = pack_half2(x.x, x.y);
-          } else {
-            const __nv_bfloat162 w = __floats2bfloat162_rn(x.x, x.y);
-            p[i] = *reinterpret_cast<const uint32_t*>(&w);
+          for (int i = 0; i < 16; ++i) {
+            float2 e = __ffma2_rn(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), sc2, nm2);
+            e.x = fast_exp2(e.x);
+            e.y = fast_exp2(e.y);
+            sum[i & 1] = __fadd2_rn(sum[i & 1], e);
+            if (MIXED && half16) {
+              p[c][i] = pack_half2(e.x, e.y);
+            } else {
+              const __nv_bfloat162 w = __floats2bfloat162_rn(e.x, e.y);
+              p[c][i] = *reinterpret_cast<const uint32_t*>(&w);
+            }
           }
         }
-        tc_st16(tS + 16 * c, p);
+        sum[0] = __fadd2_rn(sum[0], sum[1]);
+        if (fresh || !__any_sync(0xffffffffu, sum[0].x + sum[0].y > kGrown)) break;
       }
-      l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+      // P takes the columns of the scores
+      tc_st32(tS, &p[0][0]);
+      tc_st32(tS + 32, &p[2][0]);
+      l += sum[0].x + sum[0].y;
       tc_st_wait();
       ready();
       have = true;
@@ -729,13 +840,15 @@ __device__ void softmax_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, Cursor
       if (!ok) break;
       float scale = kScoreLog2;
       {
-        uint32_t s[4][32];
-        load_s(s);
+        uint32_t s[32];
         float mx = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          tc_ld32_issue(tS + 32 * c, s);
+          tc_ld_wait1(s);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(__uint_as_float(s[c][i])));
+          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(__uint_as_float(s[i])));
+        }
         const uint32_t e = __float_as_uint(mx) >> 23;
         float down = 1.f;
         if (e > 0 && e < 254) {
@@ -743,13 +856,18 @@ __device__ void softmax_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, Cursor
           scale *= __uint_as_float(e << 23);
         }
         uint8_t* q = sq + u * kTileBytes + row * 128;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          tc_ld32_issue(tS + 32 * c, s);
+          tc_ld_wait1(s);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          uint32_t w[4];
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = pack_half2(__uint_as_float(s[c >> 2][(c & 3) * 8 + 2 * i]) * down, __uint_as_float(s[c >> 2][(c & 3) * 8 + 2 * i + 1]) * down);
-          *reinterpret_cast<uint4*>(q + (c >> 3) * kHalfBytes + (((c & 7) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack_half2(__uint_as_float(s[8 * j + 2 * i]) * down, __uint_as_float(s[8 * j + 2 * i + 1]) * down);
+            *reinterpret_cast<uint4*>(q + (c >> 1) * kHalfBytes + (((4 * (c & 1) + j) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
       }
       fence_proxy_async();
@@ -759,12 +877,11 @@ __device__ void softmax_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, Cursor
       ok = wait_s();  // O is complete
       if (!ok) break;
       if (!C.P.absorbed) {
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32], hi[16], lo[16];
           tc_ld32_issue(tO + 32 * c, o);
-          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-          tc_ld_wait_pass(o);
+          tc_ld_wait1(o);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float x = __uint_as_float(o[2 * i]), y = __uint_as_float(o[2 * i + 1]);
@@ -803,14 +920,13 @@ __device__ void softmax_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, Cursor
     for (int c = 0; c < 4; ++c) {
       uint32_t o[32];
       tc_ld32_issue(tO + 32 * c, o);
-      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-      tc_ld_wait_pass(o);
+      tc_ld_wait1(o);
       if (live) {
       float f[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]);
       if (bad) {  // non-finite values this row does see
-        const int j0 = max(cur.s.A + cur.t * cur.bt + 1, 0) / kTile;
+        const int j0 = cur.keys_all() / kTile;
         for (int b = 0; b < kTile * 4; ++b) {
           const int key = j0 * kTile + b;
           if (key >= lim || !((sh->bad[sb][b >> 7][(b >> 5) & 3] >> (b & 31)) & 1)) continue;
@@ -834,19 +950,18 @@ __device__ void softmax_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, Cursor
       }
       if (whole) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t w[4];
+        for (int i = 0; i < 2; ++i) {
+          uint32_t w[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(f[8 * i + 2 * e] * inv, f[8 * i + 2 * e + 1] * inv);
+          for (int e = 0; e < 8; ++e) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(f[16 * i + 2 * e] * inv, f[16 * i + 2 * e + 1] * inv);
             w[e] = *reinterpret_cast<const uint32_t*>(&x);
           }
-          reinterpret_cast<uint4*>(dst)[4 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
+          store32(dst + 32 * c + 16 * i, w, C.wide);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          reinterpret_cast<float4*>(slot)[8 * c + i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        for (int i = 0; i < 4; ++i) store32(slot + 32 * c + 8 * i, reinterpret_cast<const uint32_t*>(f) + 8 * i, true);
       }
       }
       __syncwarp();  // the next tensor-memory load is the whole warp's
@@ -855,161 +970,162 @@ __device__ void softmax_role(const ChunkArgs& C, Shared* sh, uint8_t* sq, Cursor
 }
 
 // ---- dequantising warps (pool) -------------------------------------------------------------------
-// The four fp16 values a code can stand for in one group, as two words a byte selector picks from.
+// What turns a group's codes into fp16 values: scale and zero, or with a Lloyd-Max codebook the four
+// values as two words that a byte selector picks from (fp32 products, one rounding).
 struct Levels {
   uint32_t a, b;
 };
-__device__ __forceinline__ Levels levels(uint32_t sz, float l1, float l2) {
-  const float s = half_lo(sz), z = half_hi(sz);
+__device__ __forceinline__ Levels levels(uint32_t sz, float l1, bool table) {
   Levels r;
-  r.a = pack_half2(z, fmaf(l1, s, z));
-  r.b = pack_half2(fmaf(l2, s, z), fmaf(3.f, s, z));
+  if (table) {
+    const float s = half_lo(sz), z = half_hi(sz);
+    r.a = pack_half2(z, fmaf(l1, s, z));
+    r.b = pack_half2(fmaf(3.f - l1, s, z), fmaf(3.f, s, z));
+  } else {
+    r.a = __byte_perm(sz, sz, 0x1010);
+    r.b = __byte_perm(sz, sz, 0x3232);
+  }
   return r;
 }
-// Codes 2p of the four bytes of x (elements 0 .. 3) as two f16x2 words.
-__device__ __forceinline__ void pick4(uint32_t x, int p, const Levels& t, uint32_t& lo, uint32_t& hi) {
-  const uint32_t sel = ((x >> (2 * p)) & 0x03030303u) * 0x22u + 0x10101010u;  // nibbles 2c, 2c + 1 per code
-  lo = __byte_perm(t.a, t.b, sel);
-  hi = __byte_perm(t.a, t.b, sel >> 16);
+// Slot p (bits 2p, 2p + 1 of either 16-bit half) of x as an f16x2 pair of values. Uniform levels: the
+// code bits under the exponent of 2^(10 - 2p) are 2^(10 - 2p) + code, exactly; one subtraction and
+// one fused multiply-add (one rounding) make code * s + z.
+__device__ __forceinline__ uint32_t expand(uint32_t x, int p, const Levels& t, bool table) {
+  if (table) {
+    const uint32_t sel = ((x >> (2 * p)) & 0x00030003u) * 0x22u + 0x00100010u;  // nibbles 2c, 2c + 1 per code
+    return __byte_perm(t.a, t.b, __byte_perm(sel, 0, 0x4420));
+  }
+  const uint32_t base = (0x6400u - 0x800u * p) * 0x10001u;
+  const uint32_t h = (x & (0x00030003u << (2 * p))) | base;
+  const __half2 c = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&base));
+  const __half2 v = __hfma2(c, *reinterpret_cast<const __half2*>(&t.a), *reinterpret_cast<const __half2*>(&t.b));
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ void dequant_role(const ChunkArgs& C, Shared* sh, uint8_t* ring, Cursor<true> cur) {
-  const int x = threadIdx.x & 127;
+__device__ void dequant_role(const ChunkArgs& C, Shared<true>* sh, uint8_t* ring, const uint8_t* codes, Cursor<true> cur) {
+  const int x = threadIdx.x & 127, lane = threadIdx.x & 31;
   const DevPool& P = C.P;
-  const int ng = P.ngroups;
+  const int ng = P.ngroups, slots = code_slots(P);
   // K: thread x has token x of the block. V: a slice of 16 tokens, of it tokens 8u + 2tq + {0, 1} and
   // one half of the dims.
   const int slice = x >> 4, tq = (x >> 2) & 3, uu = (x >> 1) & 1, wh = x & 1;
-  Ring r;
+  Ring<true> r;
+  uint32_t cpos = 0;
   bool ok = true;
   auto skip = [&](int n) {  // tiles of the tensor-copy warp (see there)
     for (; n > 0; --n, ++r.pos)
       if (!wait_warp(&sh->empty[r.stage()], r.parity() ^ 1, sh, C.err)) return false;
     return true;
   };
+  auto done = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
   for (; ok && cur.valid(); cur.next(C)) {
     if (cur.empty()) continue;
     const int nI = min(cur.k1, cur.s.nI);
     if (cur.k0 < nI) {
-      ok = and128(skip(kLimbs));
-      if (!ok) break;
+      ok = skip(kLimbs);
       const size_t lh = (size_t)C.layer * P.Hkv + cur.h;
-      const float ak = P.lloyd ? P.cb_a[lh * 2] : 1.f, av = P.lloyd ? P.cb_a[lh * 2 + 1] : 1.f;
-      const float ak2 = 3.f - ak, av2 = 3.f - av;
-      const uint8_t* base = P.int2 + (size_t)C.layer * P.int2_layer_stride;
-      auto page = [&](int j) -> const uint8_t* {  // page j of the history, null when it has none
-        if (j * kPage >= cur.s.hist) return nullptr;
-        int64_t pid = P.page_table[(size_t)cur.s.seq * P.maxp + j];
-        if (pid < 0 || pid >= P.max_int2_pages) {
-          set_err(P.err, OSCAR_DEVERR_PAGE);
-          pid = 0;
-        }
-        return base + ((size_t)pid * P.Hkv + cur.h) * P.block_bytes;
-      };
-      // the packed words of one block, fetched a block ahead
-      uint4 kc[2];
-      uint32_t vc[8], ksz[4], vsz[2][2];
-      auto fetch = [&](int k) {
-        const uint8_t* kp = page(2 * k + (x >> 6));
-        const int tau = x & 63;
-        kc[0] = kc[1] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ksz[i] = 0;
-        if (kp && (2 * k + (x >> 6)) * kPage + tau < cur.s.hist) {
-          kc[0] = reinterpret_cast<const uint4*>(kp + tau * kCodeBytes)[0];
-          kc[1] = reinterpret_cast<const uint4*>(kp + tau * kCodeBytes)[1];
-          const uint32_t* sz = reinterpret_cast<const uint32_t*>(kp + 2 * kPage * kCodeBytes);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < ng) ksz[i] = sz[sz_index(tau, i, ng)];
-        }
-        // V: slices 0 .. 3 are the block's first page
-        const uint8_t* vp = page(2 * k + (slice >> 2));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) vc[i] = 0;
-        vsz[0][0] = vsz[0][1] = vsz[1][0] = vsz[1][1] = 0;
-        if (vp) {
-          const uint8_t* c = vp + kPage * kCodeBytes + (slice & 3) * 512 + tq * 16 + 8 * uu + 4 * wh;
-#pragma unroll
-          for (int g = 0; g < 8; ++g) vc[g] = *reinterpret_cast<const uint32_t*>(c + g * 64);
-          const uint32_t* sz = reinterpret_cast<const uint32_t*>(vp + 2 * kPage * kCodeBytes) + kPage * ng;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int tau2 = (slice & 3) * 16 + 8 * uu + 2 * tq + e;
-            if ((2 * k + (slice >> 2)) * kPage + tau2 < cur.s.hist) {  // else scale and zero stay 0: zero rows
-#pragma unroll
-              for (int w = 0; w < 2; ++w) vsz[e][w] = sz[sz_index(tau2, ng == 1 ? 0 : 2 * wh + w, ng)];
-            }
-          }
-        }
-      };
-      fetch(cur.k0);
+      const bool table = P.lloyd != 0;
+      const float ak = table ? P.cb_a[lh * 2] : 1.f, av = table ? P.cb_a[lh * 2 + 1] : 1.f;
       for (int k = cur.k0; ok && k < nI; ++k) {
+        const int slot = cpos % slots;
+        ok = wait_warp(&sh->code_full[slot], (cpos / slots) & 1, sh, C.err);
+        if (!ok) break;
+        ++cpos;
+        // this thread's packed words; of a token behind the history the scale and zero are 0, so its values are
+        const uint8_t* kp = codes + (size_t)(slot * 2 + (x >> 6)) * P.block_bytes;
+        const uint8_t* vp = codes + (size_t)(slot * 2 + (slice >> 2)) * P.block_bytes;
+        const uint4 kc0 = reinterpret_cast<const uint4*>(kp + (x & 63) * kCodeBytes)[0];
+        const uint4 kc1 = reinterpret_cast<const uint4*>(kp + (x & 63) * kCodeBytes)[1];
+        uint32_t vc[8], ksz[4], vsz[2][2];
+        const uint8_t* vw = vp + kPage * kCodeBytes + (slice & 3) * 512 + tq * 16 + 8 * uu + 4 * wh;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) vc[g] = *reinterpret_cast<const uint32_t*>(vw + g * 64);
+        const uint32_t* sz = reinterpret_cast<const uint32_t*>(kp + 2 * kPage * kCodeBytes);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ksz[i] = i < ng ? sz[sz_index(x & 63, i, ng)] : 0;
+        sz = reinterpret_cast<const uint32_t*>(vp + 2 * kPage * kCodeBytes) + kPage * ng;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int tau = (slice & 3) * 16 + 8 * uu + 2 * tq + e;
+          const bool live = k * kTile + (slice >> 2) * kPage + tau < cur.s.hist;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) vsz[e][w] = live ? sz[sz_index(tau, ng == 1 ? 0 : 2 * wh + w, ng)] : 0;
+        }
+        done(&sh->code_empty[slot]);
         // K tile
         int s = r.stage();
-        bool w = wait_warp(&sh->empty[s], r.parity() ^ 1, sh, C.err);
-        if (w) {
+        ok = wait_warp(&sh->empty[s], r.parity() ^ 1, sh, C.err);
+        if (!ok) break;
+        {
+          // dims 64 wd + 32 sh8 + 8p + 2tq + {0, 1} are slot p of byte sh8 of the halves of word [tq][wd]
           uint8_t* dst = ring + s * kTileBytes + x * 128;
-          const uint32_t W[8] = {kc[0].x, kc[0].y, kc[0].z, kc[0].w, kc[1].x, kc[1].y, kc[1].z, kc[1].w};  // [tq][word]
+          auto tile = [&](bool tab) {
+#pragma unroll 1
+            for (int wd = 0; wd < 2; ++wd, dst += kHalfBytes) {
+              uint32_t W[4] = {wd ? kc0.y : kc0.x, wd ? kc0.w : kc0.z, wd ? kc1.y : kc1.x, wd ? kc1.w : kc1.z};
+              Levels t = levels(ng == 1 || !wd ? ksz[0] : ksz[2], ak, tab);
 #pragma unroll
-          for (int wd = 0; wd < 2; ++wd)
+              for (int sh8 = 0; sh8 < 2; ++sh8) {
+                if (sh8) {
 #pragma unroll
-            for (int sh8 = 0; sh8 < 2; ++sh8) {
-              const Levels t = levels(ng == 1 ? ksz[0] : ksz[2 * wd + sh8], ak, ak2);
-              const uint32_t sel = sh8 ? 0x7531u : 0x6420u;
-              const uint32_t xa = __byte_perm(W[wd], W[2 + wd], sel), xb = __byte_perm(W[4 + wd], W[6 + wd], sel);
+                  for (int i = 0; i < 4; ++i) W[i] >>= 8;
+                  if (ng > 1) t = levels(wd ? ksz[3] : ksz[1], ak, tab);
+                }
 #pragma unroll
-              for (int p = 0; p < 4; ++p) {
-                uint4 v;
-                pick4(xa, p, t, v.x, v.y);
-                pick4(xb, p, t, v.z, v.w);
-                const int c = 4 * sh8 + p;  // chunk of the half wd
-                *reinterpret_cast<uint4*>(dst + wd * kHalfBytes + ((c ^ (x & 7)) << 4)) = v;
+                for (int p = 0; p < 4; ++p)  // chunk 4 sh8 + p of the half wd
+                  *reinterpret_cast<uint4*>(dst + (((4 * sh8 + p) ^ (x & 7)) << 4)) =
+                      make_uint4(expand(W[0], p, t, tab), expand(W[1], p, t, tab), expand(W[2], p, t, tab), expand(W[3], p, t, tab));
               }
             }
-          fence_proxy_async();
+          };
+          if (table) tile(true); else tile(false);
         }
-        ok = and128(w);
-        if (ok && x == 0) mbar_arrive(&sh->full[s]);
+        fence_proxy_async();
+        done(&sh->full[s]);
         ++r.pos;
-        if (!ok) break;
         // V tile
         s = r.stage();
-        w = wait_warp(&sh->empty[s], r.parity() ^ 1, sh, C.err);
-        if (w) {
+        ok = wait_warp(&sh->empty[s], r.parity() ^ 1, sh, C.err);
+        if (!ok) break;
+        {
+          // dims 32 (2 wh + w1) + 8p + g of token e are slot p of byte w1 of half e of word g
           uint8_t* half = ring + s * kTileBytes + wh * kHalfBytes;
+          auto tile = [&](bool tab) {
+#pragma unroll 1
+            for (int ee = 0; ee < 2; ++ee) {
+              const int e = ee ^ uu;  // lanes of odd u start with the odd token: eight rows, eight banks
+              const int rowv = slice * 16 + 8 * uu + 2 * tq + e;
+              uint8_t* dst = half + rowv * 128;
+              Levels t = levels(e ? vsz[1][0] : vsz[0][0], av, tab);
+              uint32_t W[4];
 #pragma unroll
-          for (int ee = 0; ee < 2; ++ee) {
-            const int e = ee ^ uu;  // lanes of odd u start with the odd token: eight rows, eight banks
-            const int rowv = slice * 16 + 8 * uu + 2 * tq + e;
+              for (int i = 0; i < 4; ++i) W[i] = __byte_perm(vc[2 * i], vc[2 * i + 1], e ? 0x7632 : 0x5410);
 #pragma unroll
-            for (int w1 = 0; w1 < 2; ++w1) {
-              const Levels t = levels(e ? vsz[1][w1] : vsz[0][w1], av, av2);
-              // byte 2e + w1 of the eight words: elements 0 .. 7 of the chunks
-              const uint32_t sel = (uint32_t)(2 * e + w1) * 0x11u + 0x40u;
-              const uint32_t x01 = __byte_perm(vc[0], vc[1], sel), x23 = __byte_perm(vc[2], vc[3], sel);
-              const uint32_t x45 = __byte_perm(vc[4], vc[5], sel), x67 = __byte_perm(vc[6], vc[7], sel);
-              const uint32_t xa = __byte_perm(x01, x23, 0x5410u), xb = __byte_perm(x45, x67, 0x5410u);
+              for (int w1 = 0; w1 < 2; ++w1) {
+                if (w1) {
 #pragma unroll
-              for (int p = 0; p < 4; ++p) {
-                uint4 v;
-                pick4(xa, p, t, v.x, v.y);
-                pick4(xb, p, t, v.z, v.w);
-                const int c = 4 * w1 + p;
-                *reinterpret_cast<uint4*>(half + rowv * 128 + ((c ^ (rowv & 7)) << 4)) = v;
+                  for (int i = 0; i < 4; ++i) W[i] >>= 8;
+                  if (ng > 1) t = levels(e ? vsz[1][1] : vsz[0][1], av, tab);
+                }
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                  *reinterpret_cast<uint4*>(dst + (((4 * w1 + p) ^ (rowv & 7)) << 4)) =
+                      make_uint4(expand(W[0], p, t, tab), expand(W[1], p, t, tab), expand(W[2], p, t, tab), expand(W[3], p, t, tab));
               }
             }
-          }
-          fence_proxy_async();
+          };
+          if (table) tile(true); else tile(false);
         }
-        if (k + 1 < nI) fetch(k + 1);
-        ok = and128(w);
-        if (ok && x == 0) mbar_arrive(&sh->full[s]);
+        fence_proxy_async();
+        done(&sh->full[s]);
         ++r.pos;
       }
-      if (ok && !P.absorbed) ok = and128(skip(kLimbs));
+      if (ok && !P.absorbed) ok = skip(kLimbs);
     }
-    if (ok) ok = and128(skip(2 * (cur.k1 - max(cur.k0, nI))));
+    if (ok) ok = skip(2 * (cur.k1 - max(cur.k0, nI)));
   }
 }
 
@@ -1026,28 +1142,46 @@ __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// Units of all sequences, and the place of unit g0(total) in them; every thread of the CTA.
+// First unit of CTA c of n.
+__device__ __forceinline__ int64_t boundary(int c, int64_t total, int n) {
+  if (c >= n) return total;
+  return total < (1 << 22) ? (int64_t)((uint32_t)c * (uint32_t)total / (uint32_t)n) : (int64_t)c * total / n;
+}
+
+// Units of all sequences, this CTA's range [g0, g1) of them and the item that holds g0; every thread
+// of the CTA. Returns the number of CTAs that have a range.
 template <bool MIXED>
-__device__ int64_t plan(const ChunkArgs& C, Shared* sh, int bt, int64_t& g0, int64_t& g1, int grid) {
+__device__ int plan(const ChunkArgs& C, Shared<MIXED>* sh, int64_t& g0, int64_t& g1) {
   constexpr int NT = kChunkThreads<MIXED>, NW = NT / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t mine = 0, total = 0;
-  for (int i = threadIdx.x; i < C.n_seqs; i += NT) mine += units_of(load_seq<MIXED>(C, i), bt) * C.Hkv;
+  // the first NT sequences stay in registers for the second pass
+  SeqWork s0{};
+  if (threadIdx.x < C.n_seqs) s0 = load_seq<MIXED>(C, threadIdx.x);
+  const int64_t per0 = units_of(s0, C.lg);
+  int64_t mine = per0 * C.Hkv, total = 0;
+  for (int i = threadIdx.x + NT; i < C.n_seqs; i += NT) mine += units_of(load_seq<MIXED>(C, i), C.lg) * C.Hkv;
 #pragma unroll
   for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) sh->scan[warp] = mine;
   __syncthreads();
+#pragma unroll
   for (int w = 0; w < NW; ++w) total += sh->scan[w];
-  const int64_t n = min((int64_t)grid, max((int64_t)1, total / kMinUnits));
-  g0 = blockIdx.x < n ? (int64_t)blockIdx.x * total / n : total;
-  g1 = blockIdx.x < n ? ((int64_t)blockIdx.x + 1) * total / n : total;
+  const int n = (int)min((int64_t)gridDim.x, max((int64_t)1, total / kMinUnits));
+  g0 = boundary(blockIdx.x, total, n);
+  g1 = boundary(blockIdx.x + 1, total, n);
   if (g0 >= g1) return n;
+  if (threadIdx.x == 0) sh->total = total;
   int64_t base = 0;
   for (int i0 = 0; i0 < C.n_seqs; i0 += NT) {
     const int i = i0 + threadIdx.x;
-    SeqWork s{};
-    if (i < C.n_seqs) s = load_seq<MIXED>(C, i);
-    const int64_t per = units_of(s, bt), cnt = per * C.Hkv;
+    SeqWork s = s0;
+    int64_t per = per0;
+    if (i0) {
+      s = SeqWork{};
+      if (i < C.n_seqs) s = load_seq<MIXED>(C, i);
+      per = units_of(s, C.lg);
+    }
+    const int64_t cnt = per * C.Hkv;
     int64_t inc = cnt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -1058,25 +1192,30 @@ __device__ int64_t plan(const ChunkArgs& C, Shared* sh, int bt, int64_t& g0, int
     if (lane == 31) sh->scan[warp] = inc;
     __syncthreads();
     int64_t before = base + inc - cnt;
-    for (int w = 0; w < warp; ++w) before += sh->scan[w];
-    for (int w = 0; w < NW; ++w) base += sh->scan[w];
+    for (int w = 0; w < NW; ++w) {
+      const int64_t y = sh->scan[w];
+      if (w < warp) before += y;
+      base += y;
+    }
     if (cnt > 0 && g0 >= before && g0 < before + cnt) {
       int64_t x = g0 - before;
-      const int h = (int)(x / per);
-      x -= h * per;
-      int lo = 0, hi = pairs_of(s, bt) - 1;
+      int h = 0;
+      while (x >= per) {
+        x -= per;
+        ++h;
+      }
+      int lo = 0, hi = pairs_of(s, C.lg) - 1;
       while (lo < hi) {  // the last pair that starts at or before x
         const int mid = (lo + hi + 1) >> 1;
-        if (units_before(s, bt, mid) <= x) lo = mid; else hi = mid - 1;
+        if (units_before(s, C.lg, mid) <= x) lo = mid; else hi = mid - 1;
       }
       sh->st_i = i;
       sh->st_h = h;
       sh->st_t = lo;
-      sh->st_k = (int)(x - units_before(s, bt, lo));
+      sh->st_x = x - units_before(s, C.lg, lo);
     }
     if (base > g0) break;
   }
-  sh->total = total;
   return n;
 }
 
@@ -1085,18 +1224,23 @@ __global__ void __launch_bounds__(kChunkThreads<MIXED>, 1)
     k_chunk(const __grid_constant__ ChunkArgs C, const __grid_constant__ ChunkMaps M) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t *sq = smem, *ring = smem + 2 * kTileBytes;
-  Shared* sh = reinterpret_cast<Shared*>(ring + kStages * kTileBytes);
+  uint8_t *sq = smem, *ring = smem + 2 * kTileBytes, *codes = ring + kStages<MIXED> * kTileBytes;
+  Shared<MIXED>* sh = reinterpret_cast<Shared<MIXED>*>(codes + (MIXED ? kCodeBuf : 0));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bt = 2 * kTile / C.hg;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sh->full[s], 1);
+    for (int s = 0; s < kStages<MIXED>; ++s) {
+      mbar_init(&sh->full[s], MIXED ? 4 : 1);
       mbar_init(&sh->empty[s], 1);
+    }
+    for (int s = 0; s < kMaxSlots; ++s) {
+      mbar_init(&sh->code_full[s], 1);
+      mbar_init(&sh->code_empty[s], 4);
     }
     mbar_init(&sh->q_full, 1);
     mbar_init(&sh->q_empty, 1);
     mbar_init(&sh->done, 1);
+    mbar_init(&sh->clean_go, 1);
+    mbar_init(&sh->clean_done, 2);
     for (int u = 0; u < 2; ++u) {
       mbar_init(&sh->s_full[u], 1);
       mbar_init(&sh->p_ready[u], kTile);
@@ -1105,7 +1249,7 @@ __global__ void __launch_bounds__(kChunkThreads<MIXED>, 1)
     fence_mbar_init();
   }
   int64_t g0, g1;
-  const int64_t n = plan<MIXED>(C, sh, bt, g0, g1, gridDim.x);
+  const int n = plan<MIXED>(C, sh, g0, g1);
   if (threadIdx.x == 0 && g0 >= g1) reinterpret_cast<Part*>(C.ws)[blockIdx.x].parts = 0;
   if (g0 >= g1) return;
   if (warp == 0) {
@@ -1116,36 +1260,43 @@ __global__ void __launch_bounds__(kChunkThreads<MIXED>, 1)
   __syncthreads();
   tc_fence_after();
   Cursor<MIXED> cur;
-  cur.start(C, sh->st_i, sh->st_h, sh->st_t, sh->st_k, g1 - g0);
+  const int64_t x0 = sh->st_x;
+  cur.start(C, sh->st_i, sh->st_h, sh->st_t, x0, g1 - g0);
   if (threadIdx.x == 0) {
-    // The item this CTA's first boundary cuts is joined by merge block blockIdx.x, if the item starts
-    // in the CTA before (else an earlier boundary cuts it too).
+    // The item this CTA's start cuts is joined by merge block blockIdx.x, if the boundary before lies in
+    // front of it (else an earlier boundary cuts it too).
     Part d{};
-    const int64_t first = g0 - cur.k0, end = first + cur.nb, c = blockIdx.x, total = sh->total;
-    if (cur.k0 > 0 && first >= (c - 1) * total / n) {
-      int64_t e = c;
-      while (e + 1 < n && (e + 1) * total / n < end) ++e;
-      d.parts = (int)(e - c + 2);
-      d.row0 = cur.s.row0 + cur.t * bt;
-      d.rows = cur.tokens() * C.hg;
-      d.head = cur.h * C.hg;
+    if (cur.k0 > 0) {
+      const int64_t total = sh->total;
+      const int64_t first = g0 - x0;
+      const int c = blockIdx.x;
+      if (cut_at(boundary(c - 1, total, n) - first, cur.nb) == 0) {
+        int e = c;
+        while (e + 1 < n && cut_at(boundary(e + 1, total, n) - first, cur.nb) < cur.nb) ++e;
+        d.parts = e - c + 2;
+        d.row0 = cur.s.row0 + (cur.t << C.lg);
+        d.rows = cur.tokens() * C.hg;
+        d.head = cur.h * C.hg;
+      }
     }
     reinterpret_cast<Part*>(C.ws)[blockIdx.x] = d;
   }
   if constexpr (MIXED) {
-    // registers of the launch: 512 x 128 = 128 x (2 x 184 + 104 + 40)
+    // registers of the launch: 512 x 128 = 128 x (2 x 184 + 88 + 56)
     if (warp < 8) {
       reg_inc<184>();
       softmax_role<true>(C, sh, sq, cur, warp >> 2);
     } else if (warp < 12) {
-      reg_dec<104>();
-      dequant_role(C, sh, ring, cur);
+      reg_dec<88>();
+      dequant_role(C, sh, ring, codes, cur);
     } else {
-      reg_dec<40>();
+      reg_dec<56>();
       if (warp == 12) {
-        if (lane == 0) load_role<true>(C, M, sh, sq, ring, cur);
+        if (lane == 0) load_role<true>(C, M, sh, sq, ring, codes, cur);
       } else if (warp == 13) {
         mma_role<true>(C, sh, sq, ring, cur, lane);
+      } else {
+        clean_role<true>(C, sh, ring, warp - 14, lane);
       }
     }
   } else {
@@ -1156,9 +1307,11 @@ __global__ void __launch_bounds__(kChunkThreads<MIXED>, 1)
     } else {
       reg_dec<88>();
       if (warp == 8) {
-        if (lane == 0) load_role<false>(C, M, sh, sq, ring, cur);
+        if (lane == 0) load_role<false>(C, M, sh, sq, ring, codes, cur);
       } else if (warp == 9) {
         mma_role<false>(C, sh, sq, ring, cur, lane);
+      } else {
+        clean_role<false>(C, sh, ring, warp - 10, lane);
       }
     }
   }
@@ -1230,6 +1383,15 @@ bool map_pages(CUtensorMap* m, const void* base, int64_t rows) {
 
 int slot_rows(int hg, int64_t n_tokens) { return n_tokens * hg <= kTile ? kTile : 2 * kTile; }
 
+int log2_of(int x) { return x <= 1 ? 0 : 1 + log2_of(x / 2); }
+
+void set_buffers(ChunkArgs& C, void* workspace, void* out) {
+  C.lg = log2_of(2 * kTile / C.hg);
+  C.out = static_cast<__nv_bfloat16*>(out);
+  C.wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+  C.ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~(uintptr_t)31);  // slots of 32-byte stores
+}
+
 int chunk_ctas() {  // one CTA per SM of the current device
   int dev = 0, sms = kMaxCtas;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
@@ -1240,9 +1402,9 @@ template <bool MIXED>
 cudaError_t launch_chunk(const ChunkArgs& C, const ChunkMaps& M, cudaStream_t s) {
   const int ctas = chunk_ctas();
   if (ctas < 1) return cudaErrorUnknown;
-  cudaError_t e = cudaFuncSetAttribute(k_chunk<MIXED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem);
+  cudaError_t e = cudaFuncSetAttribute(k_chunk<MIXED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem<MIXED>);
   if (e != cudaSuccess) return e;
-  k_chunk<MIXED><<<ctas, kChunkThreads<MIXED>, kChunkSmem, s>>>(C, M);
+  k_chunk<MIXED><<<ctas, kChunkThreads<MIXED>, kChunkSmem<MIXED>, s>>>(C, M);
   e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
   k_chunk_join<<<dim3(ctas, C.rows / kJoinRows), 256, 0, s>>>(C);
@@ -1253,7 +1415,7 @@ cudaError_t launch_chunk(const ChunkArgs& C, const ChunkMaps& M, cudaStream_t s)
 
 // Partials of a call: two slots per CTA (an item cut in front of the CTA's range, and one behind it).
 size_t chunk_workspace_bytes(int hg, int64_t n_tokens) {
-  return (size_t)kMaxCtas * (kDescBytes + 2 * (size_t)slot_rows(hg, n_tokens) * (kHeadDim + 2) * 4);
+  return 32 + (size_t)kMaxCtas * (kDescBytes + 2 * (size_t)slot_rows(hg, n_tokens) * (kHeadDim + 2) * 4);
 }
 
 cudaError_t launch_chunk_pool(const DevPool& P, const StepDims& S, int layer, const void* q, const void* k_new,
@@ -1268,8 +1430,7 @@ cudaError_t launch_chunk_pool(const DevPool& P, const StepDims& S, int layer, co
   C.P = P;
   C.layer = layer;
   C.v_new = static_cast<const __nv_bfloat16*>(v_new);
-  C.out = static_cast<__nv_bfloat16*>(out);
-  C.ws = static_cast<uint8_t*>(workspace);
+  set_buffers(C, workspace, out);
   C.err = P.err;
   ChunkMaps M;
   std::memset(&M, 0, sizeof(M));
@@ -1331,8 +1492,7 @@ oscar_status oscar_bf16_chunk(int32_t num_q_heads, int32_t num_kv_heads, int32_t
   C.v_pages = static_cast<const uint8_t*>(v_pages);
   C.max_pages = max_pages_per_seq;
   C.n_pages_total = n_pages_total;
-  C.out = static_cast<__nv_bfloat16*>(out);
-  C.ws = static_cast<uint8_t*>(workspace);
+  set_buffers(C, workspace, out);
   C.err = err;
   ChunkMaps M;
   std::memset(&M, 0, sizeof(M));
