@@ -34,6 +34,7 @@
 // a key and others do not (the diagonal), a non-finite value element is zeroed too, noted, and added
 // at the end to the rows that do see it.
 #include <cstring>
+#include <type_traits>
 
 #include "tcgen05.cuh"
 
@@ -729,7 +730,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
     float m = -INFINITY, l = 0.f;
     bool have = false;  // O holds something
 
-    auto block = [&](int k, float scale, bool half16) {
+    auto block = [&](auto half16, int k, float scale) {
       if (!wait_s()) return false;
       // scores of columns this row may not see
       uint64_t b0 = ~0ull, b1 = ~0ull;
@@ -813,7 +814,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
             e.x = fast_exp2(e.x);
             e.y = fast_exp2(e.y);
             sum[i & 1] = __fadd2_rn(sum[i & 1], e);
-            if (MIXED && half16) {
+            if constexpr (decltype(half16)::value) {
               p[c][i] = pack_half2(e.x, e.y);
             } else {
               const __nv_bfloat162 w = __floats2bfloat162_rn(e.x, e.y);
@@ -872,7 +873,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
       }
       fence_proxy_async();
       ready();
-      for (int k = cur.k0; ok && k < nI; ++k) ok = block(k, scale, true);
+      for (int k = cur.k0; ok && k < nI; ++k) ok = block(std::true_type{}, k, scale);
       if (!ok) break;
       ok = wait_s();  // O is complete
       if (!ok) break;
@@ -898,7 +899,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
       }
     }
     const int kb = max(cur.k0, nI);
-    for (int k = kb; ok && k < cur.k1; ++k) ok = block(k, kScoreLog2, false);
+    for (int k = kb; ok && k < cur.k1; ++k) ok = block(std::false_type{}, k, kScoreLog2);
     if (!ok) break;
     // O is complete (behind the last INT2 block of an absorbed pool it was waited for above)
     if (kb < cur.k1 || (MIXED && !C.P.absorbed)) ok = wait_s();
@@ -1062,26 +1063,20 @@ __device__ void dequant_role(const ChunkArgs& C, Shared<true>* sh, uint8_t* ring
         {
           // dims 64 wd + 32 sh8 + 8p + 2tq + {0, 1} are slot p of byte sh8 of the halves of word [tq][wd]
           uint8_t* dst = ring + s * kTileBytes + x * 128;
-          auto tile = [&](bool tab) {
+          auto tile = [&](auto tab) {
 #pragma unroll 1
-            for (int wd = 0; wd < 2; ++wd, dst += kHalfBytes) {
-              uint32_t W[4] = {wd ? kc0.y : kc0.x, wd ? kc0.w : kc0.z, wd ? kc1.y : kc1.x, wd ? kc1.w : kc1.z};
-              Levels t = levels(ng == 1 || !wd ? ksz[0] : ksz[2], ak, tab);
+            for (int i = 0; i < 4; ++i) {  // 64-dim half wd = i >> 1, byte sh8 = i & 1
+              uint32_t W[4] = {i & 2 ? kc0.y : kc0.x, i & 2 ? kc0.w : kc0.z, i & 2 ? kc1.y : kc1.x, i & 2 ? kc1.w : kc1.z};
 #pragma unroll
-              for (int sh8 = 0; sh8 < 2; ++sh8) {
-                if (sh8) {
+              for (int j = 0; j < 4; ++j) W[j] >>= 8 * (i & 1);
+              const Levels t = levels(ng == 1 || i == 0 ? ksz[0] : i == 1 ? ksz[1] : i == 2 ? ksz[2] : ksz[3], ak, decltype(tab)::value);
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) W[i] >>= 8;
-                  if (ng > 1) t = levels(wd ? ksz[3] : ksz[1], ak, tab);
-                }
-#pragma unroll
-                for (int p = 0; p < 4; ++p)  // chunk 4 sh8 + p of the half wd
-                  *reinterpret_cast<uint4*>(dst + (((4 * sh8 + p) ^ (x & 7)) << 4)) =
-                      make_uint4(expand(W[0], p, t, tab), expand(W[1], p, t, tab), expand(W[2], p, t, tab), expand(W[3], p, t, tab));
-              }
+              for (int p = 0; p < 4; ++p)  // chunk 4 sh8 + p of the half wd
+                *reinterpret_cast<uint4*>(dst + (i >> 1) * kHalfBytes + (((4 * (i & 1) + p) ^ (x & 7)) << 4)) =
+                    make_uint4(expand(W[0], p, t, decltype(tab)::value), expand(W[1], p, t, decltype(tab)::value), expand(W[2], p, t, decltype(tab)::value), expand(W[3], p, t, decltype(tab)::value));
             }
           };
-          if (table) tile(true); else tile(false);
+          if (table) tile(std::true_type{}); else tile(std::false_type{});
         }
         fence_proxy_async();
         done(&sh->full[s]);
@@ -1093,31 +1088,24 @@ __device__ void dequant_role(const ChunkArgs& C, Shared<true>* sh, uint8_t* ring
         {
           // dims 32 (2 wh + w1) + 8p + g of token e are slot p of byte w1 of half e of word g
           uint8_t* half = ring + s * kTileBytes + wh * kHalfBytes;
-          auto tile = [&](bool tab) {
+          auto tile = [&](auto tab) {
 #pragma unroll 1
-            for (int ee = 0; ee < 2; ++ee) {
-              const int e = ee ^ uu;  // lanes of odd u start with the odd token: eight rows, eight banks
-              const int rowv = slice * 16 + 8 * uu + 2 * tq + e;
+            for (int i = 0; i < 4; ++i) {
+              // token e, byte w1; lanes of odd u start with the odd token: eight rows, eight banks
+              const int e = (i >> 1) ^ uu, w1 = i & 1, rowv = slice * 16 + 8 * uu + 2 * tq + e;
               uint8_t* dst = half + rowv * 128;
-              Levels t = levels(e ? vsz[1][0] : vsz[0][0], av, tab);
+              const Levels t = levels(ng == 1 || !w1 ? (e ? vsz[1][0] : vsz[0][0]) : (e ? vsz[1][1] : vsz[0][1]), av, decltype(tab)::value);
+              const uint32_t sel = (e ? 0x7632u : 0x5410u);
               uint32_t W[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) W[i] = __byte_perm(vc[2 * i], vc[2 * i + 1], e ? 0x7632 : 0x5410);
+              for (int j = 0; j < 4; ++j) W[j] = __byte_perm(vc[2 * j], vc[2 * j + 1], sel) >> (8 * w1);
 #pragma unroll
-              for (int w1 = 0; w1 < 2; ++w1) {
-                if (w1) {
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) W[i] >>= 8;
-                  if (ng > 1) t = levels(e ? vsz[1][1] : vsz[0][1], av, tab);
-                }
-#pragma unroll
-                for (int p = 0; p < 4; ++p)
-                  *reinterpret_cast<uint4*>(dst + (((4 * w1 + p) ^ (rowv & 7)) << 4)) =
-                      make_uint4(expand(W[0], p, t, tab), expand(W[1], p, t, tab), expand(W[2], p, t, tab), expand(W[3], p, t, tab));
-              }
+              for (int p = 0; p < 4; ++p)
+                *reinterpret_cast<uint4*>(dst + (((4 * w1 + p) ^ (rowv & 7)) << 4)) =
+                    make_uint4(expand(W[0], p, t, decltype(tab)::value), expand(W[1], p, t, decltype(tab)::value), expand(W[2], p, t, decltype(tab)::value), expand(W[3], p, t, decltype(tab)::value));
             }
           };
-          if (table) tile(true); else tile(false);
+          if (table) tile(std::true_type{}); else tile(std::false_type{});
         }
         fence_proxy_async();
         done(&sh->full[s]);
