@@ -252,11 +252,13 @@ struct Clean {
 template <bool MIXED>
 struct Shared {
   uint64_t full[kStages<MIXED>], empty[kStages<MIXED>], code_full[kMaxSlots], code_empty[kMaxSlots];
-  uint64_t q_full, q_empty, s_full[2], p_ready[2], done, clean_go, clean_done;
+  // S of a block is followed by its P, so s_full never runs ahead of the rows' threads; O has a barrier of
+  // its own, since nothing answers it before the next S
+  uint64_t q_full, q_empty, s_full[2], p_ready[2], o_full[2], done, clean_go, clean_done;
   uint32_t tmem;
   int32_t abort;
   // plan
-  int64_t total, st_x, scan[16];
+  int64_t total, st_x, scan[20];
   int32_t st_i, st_h, st_t;
   Clean clean;
   // non-finite values of the diagonal blocks: key bits per block, two segments in turn
@@ -267,7 +269,7 @@ struct Shared {
 constexpr int kSharedBytes = 2048;
 static_assert(sizeof(Shared<true>) <= kSharedBytes && sizeof(Shared<false>) <= kSharedBytes, "Shared");
 template <bool MIXED>
-constexpr int kChunkSmem = (2 + kStages<MIXED>) * kTileBytes + (MIXED ? kCodeBuf : 0) + kSharedBytes + 1024;
+constexpr int kChunkSmem = (2 + kStages<MIXED>) * kTileBytes + (MIXED ? kCodeBuf : 0) + kSharedBytes;
 static_assert(kChunkSmem<true> <= 232448 && kChunkSmem<false> <= 232448, "shared memory of an SM");
 
 // One try that sleeps up to ns nanoseconds: a spinning warp takes issue slots from the others.
@@ -305,6 +307,15 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Shared
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
+// The ring of K / V tiles has two producers in a mixed pool: the tensor-copy warp and the four
+// dequantising warps. A parity tells a barrier's phase only to a role that is at most one phase off, so
+// both go through every position: a stage is empty again when its tile has been used (one arrival, of
+// the tensor cores) and when the producer it does not belong to has passed it (four arrivals).
+constexpr int kPassers = 4;
 template <bool MIXED>
 struct Ring {  // position in the stream of K / V tiles
   uint32_t pos = 0;
@@ -315,8 +326,7 @@ struct Ring {  // position in the stream of K / V tiles
 template <bool MIXED>
 __device__ __forceinline__ void expect_tile(uint64_t* bar, uint32_t bytes) {
   mbar_expect_tx(bar, bytes);
-  if (MIXED)
-    for (int i = 0; i < 3; ++i) mbar_arrive(bar);
+  if (MIXED) mbar_arrive_n(bar, 3);
 }
 // Blocks of packed pages that fit the code buffer.
 __device__ __forceinline__ int code_slots(const DevPool& P) { return P.ngroups == 1 ? 3 : 2; }
@@ -354,11 +364,11 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MIXED>*
     ++r.pos;
     return true;
   };
-  // Tiles that the dequantising warps fill: their stages are waited for all the same, since a parity
-  // tells the phase of a barrier only to a role that has seen every phase of it.
-  auto skip = [&](int n) {
-    for (; n > 0; --n, ++r.pos)
+  auto skip = [&](int n) {  // tiles that the dequantising warps fill
+    for (; n > 0; --n, ++r.pos) {
       if (!wait_bar<true>(&sh->empty[r.stage()], r.parity() ^ 1, sh, C.err)) return false;
+      mbar_arrive_n(&sh->empty[r.stage()], 4);
+    }
     return true;
   };
   auto load_limbs = [&](int kv) {
@@ -607,7 +617,7 @@ __device__ void mma_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq, uin
             if (u == 0 && !wait_full(vpos + 1)) return false;
             qk(u, addr(vpos + 1), idesc, false);
           }
-          commit(&sh->s_full[u]);  // the next S, or behind the last block O
+          commit(k + 1 < b ? &sh->s_full[u] : &sh->o_full[u]);  // the next S, or behind the last block O
         }
         acc = true;
         commit(&sh->empty[vpos % kStages<MIXED>]);
@@ -640,7 +650,7 @@ __device__ void mma_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq, uin
           pv(u, S(u), addr(r.pos), kIdescBf16, false);
           pv(u, S(u), addr(r.pos + 1), kIdescBf16, true);
           pv(u, S(u) + 64, addr(r.pos), kIdescBf16, true);
-          if (nI == cur.k1) commit(&sh->s_full[u]);
+          if (nI == cur.k1) commit(&sh->o_full[u]);
         }
         commit(&sh->empty[r.pos % kStages<MIXED>]);
         commit(&sh->empty[(r.pos + 1) % kStages<MIXED>]);
@@ -684,7 +694,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
   const int row = threadIdx.x & 127, warp = row >> 5;
   const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
   const uint32_t tS = sh->tmem + lane_off + u * kTile, tO = sh->tmem + lane_off + 2 * kTile + u * kTile;
-  uint32_t sn = 0, seg = 0;
+  uint32_t sn = 0, on = 0, seg = 0;
   bool ok = true;
   const int hg = C.hg, tpt = kTile / hg;
   // this warp's cursor, moved by its first lane
@@ -698,6 +708,11 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
   };
   auto wait_s = [&]() {
     const bool w = wait_warp(&sh->s_full[u], sn++ & 1, sh, C.err);
+    tc_fence_after();
+    return w;
+  };
+  auto wait_o = [&]() {
+    const bool w = wait_warp(&sh->o_full[u], on++ & 1, sh, C.err);
     tc_fence_after();
     return w;
   };
@@ -801,24 +816,24 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
         const float nm = m == -INFINITY ? 0.f : -m;
         const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
         sum[0] = sum[1] = make_float2(0.f, 0.f);
-        uint32_t x[2][32];
-        tc_ld32_issue(tS, x[0]);
+        uint32_t x[2][16];
+        tc_ld16_issue(tS, x[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t(&y)[32] = x[c & 1];
-          tc_ld_wait1(y);
-          if (c < 3) tc_ld32_issue(tS + 32 * (c + 1), x[(c + 1) & 1]);
+        for (int c = 0; c < 8; ++c) {
+          uint32_t(&y)[16] = x[c & 1];
+          tc_ld16_wait(y);
+          if (c < 7) tc_ld16_issue(tS + 16 * (c + 1), x[(c + 1) & 1]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 8; ++i) {
             float2 e = __ffma2_rn(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), sc2, nm2);
             e.x = fast_exp2(e.x);
             e.y = fast_exp2(e.y);
             sum[i & 1] = __fadd2_rn(sum[i & 1], e);
             if constexpr (decltype(half16)::value) {
-              p[c][i] = pack_half2(e.x, e.y);
+              p[c >> 1][8 * (c & 1) + i] = pack_half2(e.x, e.y);
             } else {
               const __nv_bfloat162 w = __floats2bfloat162_rn(e.x, e.y);
-              p[c][i] = *reinterpret_cast<const uint32_t*>(&w);
+              p[c >> 1][8 * (c & 1) + i] = *reinterpret_cast<const uint32_t*>(&w);
             }
           }
         }
@@ -875,7 +890,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
       ready();
       for (int k = cur.k0; ok && k < nI; ++k) ok = block(std::true_type{}, k, scale);
       if (!ok) break;
-      ok = wait_s();  // O is complete
+      ok = wait_o();  // O is complete
       if (!ok) break;
       if (!C.P.absorbed) {
 #pragma unroll 1
@@ -902,7 +917,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
     for (int k = kb; ok && k < cur.k1; ++k) ok = block(std::false_type{}, k, kScoreLog2);
     if (!ok) break;
     // O is complete (behind the last INT2 block of an absorbed pool it was waited for above)
-    if (kb < cur.k1 || (MIXED && !C.P.absorbed)) ok = wait_s();
+    if (kb < cur.k1 || (MIXED && !C.P.absorbed)) ok = wait_o();
     if (!ok) break;
 
     const bool bad = *reinterpret_cast<volatile uint32_t*>(&sh->any_bad[sb]) != 0;
@@ -1009,18 +1024,20 @@ __device__ void dequant_role(const ChunkArgs& C, Shared<true>* sh, uint8_t* ring
   const int ng = P.ngroups, slots = code_slots(P);
   // K: thread x has token x of the block. V: a slice of 16 tokens, of it tokens 8u + 2tq + {0, 1} and
   // one half of the dims.
-  const int slice = x >> 4, tq = (x >> 2) & 3, uu = (x >> 1) & 1, wh = x & 1;
+  const int slice = x >> 4, wh = (x >> 3) & 1, uu = (x >> 2) & 1, tq = x & 3;
   Ring<true> r;
   uint32_t cpos = 0;
   bool ok = true;
-  auto skip = [&](int n) {  // tiles of the tensor-copy warp (see there)
-    for (; n > 0; --n, ++r.pos)
-      if (!wait_warp(&sh->empty[r.stage()], r.parity() ^ 1, sh, C.err)) return false;
-    return true;
-  };
   auto done = [&](uint64_t* bar) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
+  };
+  auto skip = [&](int n) {  // tiles of the tensor-copy warp
+    for (; n > 0; --n, ++r.pos) {
+      if (!wait_warp(&sh->empty[r.stage()], r.parity() ^ 1, sh, C.err)) return false;
+      done(&sh->empty[r.stage()]);
+    }
+    return true;
   };
   for (; ok && cur.valid(); cur.next(C)) {
     if (cur.empty()) continue;
@@ -1210,15 +1227,14 @@ __device__ int plan(const ChunkArgs& C, Shared<MIXED>* sh, int64_t& g0, int64_t&
 template <bool MIXED>
 __global__ void __launch_bounds__(kChunkThreads<MIXED>, 1)
     k_chunk(const __grid_constant__ ChunkArgs C, const __grid_constant__ ChunkMaps M) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) uint8_t smem[];  // tiles start on the swizzle's 1024-byte boundaries
   uint8_t *sq = smem, *ring = smem + 2 * kTileBytes, *codes = ring + kStages<MIXED> * kTileBytes;
   Shared<MIXED>* sh = reinterpret_cast<Shared<MIXED>*>(codes + (MIXED ? kCodeBuf : 0));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages<MIXED>; ++s) {
       mbar_init(&sh->full[s], MIXED ? 4 : 1);
-      mbar_init(&sh->empty[s], 1);
+      mbar_init(&sh->empty[s], MIXED ? 1 + kPassers : 1);
     }
     for (int s = 0; s < kMaxSlots; ++s) {
       mbar_init(&sh->code_full[s], 1);
@@ -1231,6 +1247,7 @@ __global__ void __launch_bounds__(kChunkThreads<MIXED>, 1)
     mbar_init(&sh->clean_done, 2);
     for (int u = 0; u < 2; ++u) {
       mbar_init(&sh->s_full[u], 1);
+      mbar_init(&sh->o_full[u], 1);
       mbar_init(&sh->p_ready[u], kTile);
     }
     sh->abort = 0;
@@ -1270,15 +1287,15 @@ __global__ void __launch_bounds__(kChunkThreads<MIXED>, 1)
     reinterpret_cast<Part*>(C.ws)[blockIdx.x] = d;
   }
   if constexpr (MIXED) {
-    // registers of the launch: 512 x 128 = 128 x (2 x 184 + 88 + 56)
+    // registers of the launch: 512 x 128 = 128 x (2 x 168 + 96 + 80)
     if (warp < 8) {
-      reg_inc<184>();
+      reg_inc<168>();
       softmax_role<true>(C, sh, sq, cur, warp >> 2);
     } else if (warp < 12) {
-      reg_dec<88>();
+      reg_dec<96>();
       dequant_role(C, sh, ring, codes, cur);
     } else {
-      reg_dec<56>();
+      reg_dec<80>();
       if (warp == 12) {
         if (lane == 0) load_role<true>(C, M, sh, sq, ring, codes, cur);
       } else if (warp == 13) {
