@@ -774,13 +774,13 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
           for (int i = 0; i < 32; ++i)
             if (!((b >> i) & 1)) x[i] = 0xFF800000u;
           tc_st32(tS + 32 * c, x);
+          tc_st_wait();
         }
-        tc_st_wait();
       }
       // The maximum is taken anew only where it must be: for the rows' first block, and when the weights
       // under the last one sum to more than kGrown (they are finite then, or their sum is infinite), in
       // which case they are made again.
-      uint32_t p[4][16];
+      uint32_t p[64];
       float2 sum[2];
       for (bool fresh = __any_sync(0xffffffffu, m == -INFINITY);; fresh = true) {
         if (fresh) {
@@ -809,6 +809,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
               tc_st32(tO + 32 * c, o);
+              tc_st_wait();
             }
           }
         }
@@ -830,10 +831,10 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
             e.y = fast_exp2(e.y);
             sum[i & 1] = __fadd2_rn(sum[i & 1], e);
             if constexpr (decltype(half16)::value) {
-              p[c >> 1][8 * (c & 1) + i] = pack_half2(e.x, e.y);
+              p[8 * c + i] = pack_half2(e.x, e.y);
             } else {
               const __nv_bfloat162 w = __floats2bfloat162_rn(e.x, e.y);
-              p[c >> 1][8 * (c & 1) + i] = *reinterpret_cast<const uint32_t*>(&w);
+              p[8 * c + i] = *reinterpret_cast<const uint32_t*>(&w);
             }
           }
         }
@@ -841,8 +842,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
         if (fresh || !__any_sync(0xffffffffu, sum[0].x + sum[0].y > kGrown)) break;
       }
       // P takes the columns of the scores
-      tc_st32(tS, &p[0][0]);
-      tc_st32(tS + 32, &p[2][0]);
+      tc_st64(tS, p);
       l += sum[0].x + sum[0].y;
       tc_st_wait();
       ready();
@@ -907,9 +907,10 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
             lo[i] = *reinterpret_cast<const uint32_t*>(&b);
           }
           tc_st16(tS + 16 * c, hi);
+          tc_st_wait();
           tc_st16(tS + 64 + 16 * c, lo);
+          tc_st_wait();
         }
-        tc_st_wait();
         ready();
       }
     }
