@@ -670,6 +670,19 @@ __device__ void mma_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq, uin
   mbar_wait(&sh->done, 0, C.err);
 }
 
+// Two values in a word, fp16 or bf16.
+template <bool HALF>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  if (HALF) return pack_half2(x, y);
+  const __nv_bfloat162 w = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&w);
+}
+template <bool HALF>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if (HALF) return half2_to_float2(w);
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
 // ---- softmax warps: one thread per row -----------------------------------------------------------
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -777,73 +790,87 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
           tc_st_wait();
         }
       }
-      // The maximum is taken anew only where it must be: for the rows' first block, and when the weights
-      // under the last one sum to more than kGrown (they are finite then, or their sum is infinite), in
-      // which case they are made again.
-      uint32_t p[64];
-      float2 sum[2];
-      for (bool fresh = __any_sync(0xffffffffu, m == -INFINITY);; fresh = true) {
-        if (fresh) {
-          float mx0 = -INFINITY, mx1 = -INFINITY;
+      // The maximum is taken anew only where it must be: for the rows' first block, and when the weights of
+      // 32 scores under the last one sum to more than kGrown (each is finite then, or their sum infinite).
+      // The weights already made are scaled then, as the sums and O are. The loops stay rolled: the warps'
+      // instructions come from one cache, and unrolled they waited for it longer than for their data.
+      float2 sum = make_float2(0.f, 0.f);
+      auto grow = [&](int c0) {
+        float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll 1
+        for (int c = c0; c < 4; ++c) {
+          uint32_t x[32];
+          tc_ld32_issue(tS + 32 * c, x);
+          tc_ld_wait1(x);
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            mx0 = max3(mx0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            mx1 = max3(mx1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+          }
+        }
+        const float mb = fmaxf(mx0, mx1) * scale;
+        const float mn = fmaxf(m, mb), alpha = mb > m ? fast_exp2(m - mn) : 1.f;
+        m = mn;
+        l *= alpha;
+        sum.x *= alpha;
+        sum.y *= alpha;
+#pragma unroll 1
+        for (int c = 0; c < c0; ++c) {
+          uint32_t w[16];
+          tc_ld16_issue(tS + 16 * c, w);
+          tc_ld16_wait(w);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 f = unpack2<decltype(half16)::value>(w[i]);
+            w[i] = pack2<decltype(half16)::value>(f.x * alpha, f.y * alpha);
+          }
+          tc_st16(tS + 16 * c, w);
+          tc_st_wait();
+        }
+        if (have) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            uint32_t x[32];
-            tc_ld32_issue(tS + 32 * c, x);
-            tc_ld_wait1(x);
+            uint32_t o[32];
+            tc_ld32_issue(tO + 32 * c, o);
+            tc_ld_wait1(o);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              mx0 = max3(mx0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-              mx1 = max3(mx1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
-            }
-          }
-          const float mb = fmaxf(mx0, mx1) * scale;
-          const float mn = fmaxf(m, mb), alpha = mb > m ? fast_exp2(m - mn) : 1.f;
-          m = mn;
-          l *= alpha;
-          if (have) {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tc_ld32_issue(tO + 32 * c, o);
-              tc_ld_wait1(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tc_st32(tO + 32 * c, o);
-              tc_st_wait();
-            }
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tc_st32(tO + 32 * c, o);
+            tc_st_wait();
           }
         }
-        // two scores an instruction, but for the exponentials
-        const float nm = m == -INFINITY ? 0.f : -m;
-        const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(nm, nm);
-        sum[0] = sum[1] = make_float2(0.f, 0.f);
-        uint32_t x[2][16];
-        tc_ld16_issue(tS, x[0]);
+      };
+      bool fresh = __any_sync(0xffffffffu, m == -INFINITY);
+      if (fresh) grow(0);
+      const float2 sc2 = make_float2(scale, scale);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32], p[16];
+        float2 s0, s1;
+        tc_ld32_issue(tS + 32 * c, x);
+        tc_ld_wait1(x);
+        for (;;) {
+          // two scores an instruction, but for the exponentials
+          const float nm = m == -INFINITY ? 0.f : -m;
+          const float2 nm2 = make_float2(nm, nm);
+          s0 = s1 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t(&y)[16] = x[c & 1];
-          tc_ld16_wait(y);
-          if (c < 7) tc_ld16_issue(tS + 16 * (c + 1), x[(c + 1) & 1]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float2 e = __ffma2_rn(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), sc2, nm2);
+          for (int i = 0; i < 16; ++i) {
+            float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc2, nm2);
             e.x = fast_exp2(e.x);
             e.y = fast_exp2(e.y);
-            sum[i & 1] = __fadd2_rn(sum[i & 1], e);
-            if constexpr (decltype(half16)::value) {
-              p[8 * c + i] = pack_half2(e.x, e.y);
-            } else {
-              const __nv_bfloat162 w = __floats2bfloat162_rn(e.x, e.y);
-              p[8 * c + i] = *reinterpret_cast<const uint32_t*>(&w);
-            }
+            if (i & 1) s1 = __fadd2_rn(s1, e); else s0 = __fadd2_rn(s0, e);
+            p[i] = pack2<decltype(half16)::value>(e.x, e.y);
           }
+          s0 = __fadd2_rn(s0, s1);
+          if (fresh || !__any_sync(0xffffffffu, s0.x + s0.y > kGrown)) break;
+          grow(c);
+          fresh = true;
         }
-        sum[0] = __fadd2_rn(sum[0], sum[1]);
-        if (fresh || !__any_sync(0xffffffffu, sum[0].x + sum[0].y > kGrown)) break;
+        sum = __fadd2_rn(sum, s0);
+        tc_st16(tS + 16 * c, p);  // the columns of scores already read
       }
-      // P takes the columns of the scores
-      tc_st64(tS, p);
-      l += sum[0].x + sum[0].y;
+      l += sum.x + sum.y;
       tc_st_wait();
       ready();
       have = true;
