@@ -243,10 +243,11 @@ __device__ __forceinline__ uint64_t bits(int lo, int hi) {  // bits [lo, hi) of 
 }
 
 // ------------------------------------------------------------------------------------------------
-// A V tile to be cleaned: rows outside live are zeroed, rows [lo, hi) searched for non-finite values.
+// A V tile to be cleaned, two halves of 64 rows: rows outside [a, b) of a half are zeroed, rows [lo, hi)
+// of the tile searched for non-finite values.
 struct Clean {
-  uint64_t live0, live1;
-  int32_t stage, lo, hi, slot;  // slot: row of `bad` that takes the keys found; stage -1: no more
+  int32_t a[2], b[2], lo, hi;
+  int32_t stage, slot;  // slot: row of `bad` that takes the keys found; stage -1: no more
 };
 
 template <bool MIXED>
@@ -488,6 +489,10 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MIXED>*
   }
 }
 
+// Bits 15 and 31: which of the two bf16 values of a word are infinite or NaN (all exponent bits set, so
+// that one more carries out).
+__device__ __forceinline__ uint32_t nonfinite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
 // ---- cleaning warps (two): a V tile at a time, 64 rows each, while the tile's scores become P ------
 template <bool MIXED>
 __device__ void clean_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* ring, int part, int lane) {
@@ -495,37 +500,44 @@ __device__ void clean_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* ring,
     if (!wait_warp<true>(&sh->clean_go, n & 1, sh, C.err)) return;
     const Clean w = sh->clean;
     if (w.stage < 0) return;
-    const uint64_t live = part ? w.live1 : w.live0;
-    const int lo = min(max(w.lo - 64 * part, 0), 64), hi = min(max(w.hi - 64 * part, 0), 64);
+    const int a = w.a[part], b = w.b[part], lo = min(max(w.lo - 64 * part, 0), 64), hi = min(max(w.hi - 64 * part, 0), 64);
     // a lane takes one 16-byte chunk of every other row
-    const int c = lane & 15;
+    const int c = lane & 15, odd = lane >> 4;
     uint8_t* base = ring + w.stage * kTileBytes + (c >> 3) * kHalfBytes + part * kPageHalfBytes + (c & 7) * 16;
-    if (live != ~0ull)
-      for (int row = lane >> 4; row < 64; row += 2)
-        if (!((live >> row) & 1)) *reinterpret_cast<uint4*>(base + row * 128) = make_uint4(0, 0, 0, 0);
-    uint32_t bad0 = 0, bad1 = 0;
-#pragma unroll 8
-    for (int row = lo + (lane >> 4); row < hi; row += 2) {
-      uint4* p = reinterpret_cast<uint4*>(base + row * 128);
-      uint4 v = *p;
-      uint32_t e[4] = {v.x, v.y, v.z, v.w};
-      uint32_t keep[4], any = 0;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int row = odd; row < a; row += 2) *reinterpret_cast<uint4*>(base + row * 128) = zero;
+#pragma unroll 4
+    for (int row = b + odd; row < 64; row += 2) *reinterpret_cast<uint4*>(base + row * 128) = zero;
+    uint32_t found[2] = {0, 0};
+    for (int r0 = lo + odd; r0 < hi; r0 += 16) {
+      uint4 v[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        keep[i] = ((e[i] & 0x7F80u) == 0x7F80u ? 0u : 0xFFFFu) | ((e[i] & 0x7F800000u) == 0x7F800000u ? 0u : 0xFFFF0000u);
-        any |= ~keep[i];
-      }
+      for (int i = 0; i < 8; ++i) v[i] = r0 + 2 * i < hi ? *reinterpret_cast<const uint4*>(base + (r0 + 2 * i) * 128) : zero;
+      uint32_t any = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) any |= nonfinite(v[i].x) | nonfinite(v[i].y) | nonfinite(v[i].z) | nonfinite(v[i].w);
       if (any) {
-        *p = make_uint4(e[0] & keep[0], e[1] & keep[1], e[2] & keep[2], e[3] & keep[3]);
-        bad0 |= row < 32 ? 1u << row : 0;
-        bad1 |= row < 32 ? 0 : 1u << (row - 32);
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const int row = r0 + 2 * i;
+          if (row >= hi) break;
+          uint32_t* e = reinterpret_cast<uint32_t*>(base + row * 128);
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t f = nonfinite(e[j]);
+            if (f) {
+              e[j] &= (f & 0x8000u ? 0u : 0xFFFFu) | (f & 0x80000000u ? 0u : 0xFFFF0000u);
+              if (row < 32) found[0] |= 1u << row; else found[1] |= 1u << (row - 32);
+            }
+          }
+        }
       }
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t b = __reduce_or_sync(0xffffffffu, i ? bad1 : bad0);
-      if (b && lane == 0) {
-        sh->bad[w.slot >> 2][w.slot & 3][2 * part + i] = b;
+      const uint32_t f = __reduce_or_sync(0xffffffffu, found[i]);
+      if (f && lane == 0) {
+        sh->bad[w.slot >> 2][w.slot & 3][2 * part + i] = f;
         sh->any_bad[w.slot >> 2] = 1;
       }
     }
@@ -589,23 +601,22 @@ __device__ void mma_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq, uin
         if (!wait_full(vpos)) return false;
         bool dirty = false;
         if (idesc == kIdescBf16) {
-          uint64_t l0, l1;
-          int lo = kTile, hi = kTile, slot = 0;
+          Clean w;
+          w.lo = w.hi = w.slot = 0;
           if (MIXED && k < cur.s.nI + cur.s.nB) {
             const Half h0 = half_of<MIXED>(cur.s, k, 0), h1 = half_of<MIXED>(cur.s, k, 1);
-            l0 = bits(h0.lo, h0.hi);
-            l1 = bits(h1.lo, h1.hi);
+            w.a[0] = h0.lo, w.b[0] = h0.hi, w.a[1] = h1.lo, w.b[1] = h1.hi;
           } else {  // the diagonal: some rows of the pair see a key and others do not
             const int j = k - cur.s.nI - cur.s.nB;
-            lo = min(max(cur.keys_all() - j * kTile, 0), kTile);
-            hi = min(cur.keys_any() - j * kTile, kTile);
-            l0 = bits(0, min(hi, 64));
-            l1 = bits(0, max(hi - 64, 0));
-            slot = 4 * sb + j - cur.keys_all() / kTile;
+            w.lo = min(max(cur.keys_all() - j * kTile, 0), kTile);
+            w.hi = min(cur.keys_any() - j * kTile, kTile);
+            w.a[0] = w.a[1] = 0, w.b[0] = min(w.hi, 64), w.b[1] = max(w.hi - 64, 0);
+            w.slot = 4 * sb + j - cur.keys_all() / kTile;
           }
-          dirty = (l0 & l1) != ~0ull || lo < hi;
+          dirty = w.lo < w.hi || w.a[0] > 0 || w.a[1] > 0 || w.b[0] < 64 || w.b[1] < 64;
           if (dirty && lane == 0) {
-            sh->clean = {l0, l1, (int)(vpos % kStages<MIXED>), lo, hi, slot};
+            w.stage = vpos % kStages<MIXED>;
+            sh->clean = w;
             mbar_arrive(&sh->clean_go);
           }
         }
@@ -841,19 +852,25 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
         }
       };
       bool fresh = __any_sync(0xffffffffu, m == -INFINITY);
-      if (fresh) grow(0);
       const float2 sc2 = make_float2(scale, scale);
+      if constexpr (MIXED) {
+      bool again = fresh;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t x[32], p[16];
-        float2 s0, s1;
-        tc_ld32_issue(tS + 32 * c, x);
-        tc_ld_wait1(x);
-        for (;;) {
+      for (int c = 0;;) {
+        if (again) {
+          grow(c);
+          fresh = true;
+          again = false;
+        }
+        const float nm = m == -INFINITY ? 0.f : -m;
+        const float2 nm2 = make_float2(nm, nm);
+#pragma unroll 1
+        for (; c < 4; ++c) {
+          uint32_t x[32], p[16];
+          float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+          tc_ld32_issue(tS + 32 * c, x);
+          tc_ld_wait1(x);
           // two scores an instruction, but for the exponentials
-          const float nm = m == -INFINITY ? 0.f : -m;
-          const float2 nm2 = make_float2(nm, nm);
-          s0 = s1 = make_float2(0.f, 0.f);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc2, nm2);
@@ -863,12 +880,40 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
             p[i] = pack2<decltype(half16)::value>(e.x, e.y);
           }
           s0 = __fadd2_rn(s0, s1);
-          if (fresh || !__any_sync(0xffffffffu, s0.x + s0.y > kGrown)) break;
-          grow(c);
-          fresh = true;
+          again = !fresh && __any_sync(0xffffffffu, s0.x + s0.y > kGrown);
+          if (again) break;
+          sum = __fadd2_rn(sum, s0);
+          tc_st16(tS + 16 * c, p);  // the columns of scores already read
         }
-        sum = __fadd2_rn(sum, s0);
-        tc_st16(tS + 16 * c, p);  // the columns of scores already read
+        if (!again) break;
+      }
+      } else {
+        uint32_t p[64];
+        for (;; fresh = true) {
+          if (fresh) grow(0);
+          const float nm = m == -INFINITY ? 0.f : -m;
+          const float2 nm2 = make_float2(nm, nm);
+          float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+          uint32_t x[2][16];
+          tc_ld16_issue(tS, x[0]);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t(&y)[16] = x[c & 1];
+            tc_ld16_wait(y);
+            if (c < 7) tc_ld16_issue(tS + 16 * (c + 1), x[(c + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float2 e = __ffma2_rn(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), sc2, nm2);
+              e.x = fast_exp2(e.x);
+              e.y = fast_exp2(e.y);
+              if (i & 1) s1 = __fadd2_rn(s1, e); else s0 = __fadd2_rn(s0, e);
+              p[8 * c + i] = pack2<decltype(half16)::value>(e.x, e.y);
+            }
+          }
+          sum = __fadd2_rn(s0, s1);
+          if (fresh || !__any_sync(0xffffffffu, sum.x + sum.y > kGrown)) break;
+        }
+        tc_st64(tS, p);
       }
       l += sum.x + sum.y;
       tc_st_wait();
