@@ -52,8 +52,11 @@ constexpr int kMaxCtas = 152;
 constexpr int kPageHalfBytes = kPage * 128;   // 64 dims of one page
 constexpr float kGrown = 16384.f;             // a block's weights under an old maximum: fp16 holds each of them
 constexpr int kDescBytes = 32;
-constexpr int kItemUnits = 2;                 // what an item costs besides its blocks (queries in, output out, pipeline)
-constexpr int kMinUnits = 4;                  // units per CTA, at least, before a call is cut further
+// Work is counted in thousands of SM cycles, as measured on batches of equal items (G = 128, hg = 4):
+// a block of BF16 keys takes 3, one of INT2 keys 4; an item takes another 6 a tile (queries in, first
+// and masked blocks, output out), and 8 more a tile for its two rotations.
+constexpr int kUnitsBf16 = 3, kUnitsInt2 = 4, kUnitsTile = 6, kUnitsRotate = 8;
+constexpr int kMinUnits = 12;                 // per CTA, at least, before a call is cut further
 
 constexpr uint32_t kIdescBase = (1u << 4) | ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
 constexpr uint32_t kIdescBf16 = kIdescBase | (1u << 7) | (1u << 10);  // A, B bf16; fp16 without these bits
@@ -137,26 +140,43 @@ __device__ __forceinline__ int real_blocks(const SeqWork& s, int lg, int t) {
   return s.nI + s.nB + (keys > 0 ? (keys + kTile - 1) / kTile : 0);
 }
 
-// Units of the tile pairs 0 .. t-1, all of them full (2^lg tokens, 16 to 256):
-// sum over u < t of max(1, pre + ceil((A + 2^lg (u + 1)) / 128)) + kItemUnits.
+__device__ __forceinline__ int pairs_of(const SeqWork& s, int lg) { return (s.n + (1 << lg) - 1) >> lg; }
+__device__ __forceinline__ int item_overhead(const SeqWork& s, int tiles) {
+  return tiles * (kUnitsTile + (s.nI > 0 ? kUnitsRotate : 0));
+}
+__device__ __forceinline__ int item_tiles(const SeqWork& s, int lg, int t) { return s.n - (t << lg) > (1 << lg) / 2 ? 2 : 1; }
+// Units of an item of nb blocks (an item without keys counts one).
+__device__ __forceinline__ int64_t item_units(const SeqWork& s, int tiles, int nb) {
+  return item_overhead(s, tiles) + (int64_t)s.nI * kUnitsInt2 + (int64_t)(nb - s.nI) * kUnitsBf16;
+}
+// Units of the tile pairs 0 .. t-1, all of them full (2^lg tokens, 16 to 256): their overheads and
+// leading blocks, and the causal blocks sum over u < t of max(1, ceil((A + 2^lg (u + 1)) / 128)).
 __device__ __forceinline__ int64_t units_before(const SeqWork& s, int lg, int t) {
   const int bt = 1 << lg;
   const int n0 = s.A < 0 ? min(-s.A >> lg, t) : 0;  // pairs without a key
   const int m = t - n0, c = s.A + (n0 << lg) + bt + kTile - 1;
-  const int64_t sum = (int64_t)n0 + (int64_t)t * kItemUnits + (int64_t)m * (s.nI + s.nB + (c >> 7));
-  if (bt >= kTile) return sum + (int64_t)(bt >> 7) * (((int64_t)m * (m - 1)) >> 1);
-  const int lr = 7 - lg, r = 1 << lr, w0 = (kTile - (c & 127) + bt - 1) >> lg;  // remainders >= w0 carry
-  const int64_t M = m >> lr;
-  const int rem = m & (r - 1);
-  return sum + r * ((M * (M - 1)) >> 1) + M * (r - w0) + rem * M + max(0, rem - w0);
+  int64_t blocks = (int64_t)n0 + (int64_t)m * (c >> 7);
+  if (bt >= kTile) {
+    blocks += (int64_t)(bt >> 7) * (((int64_t)m * (m - 1)) >> 1);
+  } else {
+    const int lr = 7 - lg, r = 1 << lr, w0 = (kTile - (c & 127) + bt - 1) >> lg;  // remainders >= w0 carry
+    const int64_t M = m >> lr;
+    const int rem = m & (r - 1);
+    blocks += r * ((M * (M - 1)) >> 1) + M * (r - w0) + rem * M + max(0, rem - w0);
+  }
+  return t * item_units(s, 2, s.nI + s.nB) + blocks * kUnitsBf16;
 }
-__device__ __forceinline__ int pairs_of(const SeqWork& s, int lg) { return (s.n + (1 << lg) - 1) >> lg; }
 __device__ __forceinline__ int64_t units_of(const SeqWork& s, int lg) {  // of one KV head
   const int T = pairs_of(s, lg);
-  return T ? units_before(s, lg, T - 1) + max(1, real_blocks(s, lg, T - 1)) + kItemUnits : 0;
+  return T ? units_before(s, lg, T - 1) + item_units(s, item_tiles(s, lg, T - 1), max(1, real_blocks(s, lg, T - 1))) : 0;
 }
-// The block in front of which a boundary x units behind an item's start cuts it.
-__device__ __forceinline__ int cut_at(int64_t x, int nb) { return (int)min((int64_t)nb, max((int64_t)0, x - kItemUnits / 2)); }
+// The block in front of which a boundary x units behind an item's start cuts it (never one block off
+// either end).
+__device__ __forceinline__ int cut_at(const SeqWork& s, int tiles, int64_t x, int nb) {
+  const int64_t y = x - item_overhead(s, tiles) / 2, yi = (int64_t)s.nI * kUnitsInt2;
+  const int64_t k = y <= 0 ? 0 : y < yi ? y / kUnitsInt2 : s.nI + (y - yi) / kUnitsBf16;
+  return k < 2 ? 0 : k > nb - 2 ? nb : (int)k;
+}
 
 // A place in the order (sequence, KV head, tile pair, block), moved segment by segment up to the
 // CTA's end.
@@ -175,15 +195,15 @@ struct Cursor {
     end = x + n;
     s = load_seq<MIXED>(C, i);
     nb = max(1, real_blocks(s, lg, t));
-    k0 = cut_at(x, nb);
-    k1 = cut_at(end, nb);
+    k0 = cut_at(s, tiles(), x, nb);
+    k1 = cut_at(s, tiles(), end, nb);
     if (k0 >= nb) next(C);
   }
   __device__ __forceinline__ bool valid() const { return k1 > k0; }
   __device__ __forceinline__ void next(const ChunkArgs& C) {
-    end -= nb + kItemUnits;
+    end -= item_units(s, tiles(), nb);
     k0 = k1 = 0;
-    if (end <= kItemUnits / 2) return;
+    if (end <= 0) return;
     if (++t >= pairs_of(s, lg)) {
       t = 0;
       if (++h >= C.Hkv) {
@@ -195,11 +215,12 @@ struct Cursor {
       }
     }
     nb = max(1, real_blocks(s, lg, t));
-    k1 = cut_at(end, nb);
+    k1 = cut_at(s, tiles(), end, nb);
   }
   __device__ __forceinline__ bool empty() const { return real_blocks(s, lg, t) == 0; }
   __device__ __forceinline__ int tokens() const { return min(1 << lg, s.n - (t << lg)); }
-  __device__ __forceinline__ bool two() const { return tokens() > (1 << lg) / 2; }  // the second tile has rows
+  __device__ __forceinline__ int tiles() const { return item_tiles(s, lg, t); }
+  __device__ __forceinline__ bool two() const { return tiles() == 2; }  // the second tile has rows
   // Causal keys that every row of the pair sees, and that any does.
   __device__ __forceinline__ int keys_all() const { return max(s.A + (t << lg) + 1, 0); }
   __device__ __forceinline__ int keys_any() const { return s.A + min(s.n, (t + 1) << lg); }
@@ -1348,9 +1369,9 @@ __global__ void __launch_bounds__(kChunkThreads<MIXED>, 1)
       const int64_t total = sh->total;
       const int64_t first = g0 - x0;
       const int c = blockIdx.x;
-      if (cut_at(boundary(c - 1, total, n) - first, cur.nb) == 0) {
+      if (cut_at(cur.s, cur.tiles(), boundary(c - 1, total, n) - first, cur.nb) == 0) {
         int e = c;
-        while (e + 1 < n && cut_at(boundary(e + 1, total, n) - first, cur.nb) < cur.nb) ++e;
+        while (e + 1 < n && cut_at(cur.s, cur.tiles(), boundary(e + 1, total, n) - first, cur.nb) < cur.nb) ++e;
         d.parts = e - c + 2;
         d.row0 = cur.s.row0 + (cur.t << C.lg);
         d.rows = cur.tokens() * C.hg;
