@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
-from .pool import HEAD_DIM, _need, _stream
+from .pool import HEAD_DIM, _need, _on_current_device, _raw_stream
 from .rope import _rows
 
 PAGE = 64
@@ -28,14 +28,17 @@ def bf16_chunk_attend(q, k_pages, v_pages, page_table, lengths, cu_tokens, err, 
     _need(lengths, torch.int32, (seqs,), "lengths")
     _need(cu_tokens, torch.int32, (seqs + 1,), "cu_tokens")
     _need(err, torch.int32, (1,), "err")
-    nb = B.oscar_bf16_chunk_workspace_bytes(hq, hkv, seqs, n)
+    lib = B.lib()
     if workspace is None:
-        workspace = torch.empty(max(nb, 16), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(max(lib.oscar_bf16_chunk_workspace_bytes(hq, hkv, seqs, n), 16), dtype=torch.uint8, device=q.device)
     if out is None:
         out = torch.empty((n, hq, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
-    _need(out, torch.bfloat16, (n, hq, HEAD_DIM), "out")
-    B.oscar_bf16_chunk(hq, hkv, seqs, n, k_pages, v_pages, pages, page_table, width, lengths, cu_tokens, q, stride,
-                       workspace, workspace.numel() * workspace.element_size(), out, err, _stream())
+    else:
+        _need(out, torch.bfloat16, (n, hq, HEAD_DIM), "out")
+    B._check("oscar_bf16_chunk", lib.oscar_bf16_chunk(
+        hq, hkv, seqs, n, k_pages.data_ptr(), v_pages.data_ptr(), pages, page_table.data_ptr(), width, lengths.data_ptr(),
+        cu_tokens.data_ptr(), q.data_ptr(), stride, workspace.data_ptr(), workspace.nbytes, out.data_ptr(), err.data_ptr(),
+        _raw_stream()))
     return out
 
 
@@ -50,6 +53,6 @@ def bf16_copy_pages(k_pages, v_pages, src, dst):
     pages, hkv = shape[-4], shape[-3]
     _need(k_pages, torch.bfloat16, tuple(shape[:-2]) + (PAGE, HEAD_DIM), "k_pages")
     _need(v_pages, torch.bfloat16, tuple(shape), "v_pages")
-    if k_pages.device.index != torch.cuda.current_device():
+    if not _on_current_device(k_pages):
         raise ValueError("k_pages must be on the current CUDA device")
-    B.oscar_bf16_copy_pages(hkv, layers, pages * hkv * PAGE * HEAD_DIM * 2, k_pages, v_pages, pages, src, dst, _stream())
+    B.oscar_bf16_copy_pages(hkv, layers, pages * hkv * PAGE * HEAD_DIM * 2, k_pages, v_pages, pages, src, dst, _raw_stream())

@@ -33,6 +33,7 @@
 // NaN: such values are zeroed in shared memory before the product. Where some rows of the tile see
 // a key and others do not (the diagonal), a non-finite value element is zeroed too, noted, and added
 // at the end to the rows that do see it.
+#include <atomic>
 #include <cstring>
 #include <type_traits>
 
@@ -1491,20 +1492,29 @@ void set_buffers(ChunkArgs& C, void* workspace, void* out) {
   C.ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~(uintptr_t)31);  // slots of 32-byte stores
 }
 
-int chunk_ctas() {  // one CTA per SM of the current device
-  int dev = 0, sms = kMaxCtas;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return sms < kMaxCtas ? sms : kMaxCtas;
+// One CTA per SM of the current device (0: a CUDA call failed); the kernel's shared memory is asked
+// for on the first call per device.
+template <bool MIXED>
+int chunk_ctas() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> ctas[kDevices];  // 0: not set up
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < kDevices && (sms = ctas[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      cudaFuncSetAttribute(k_chunk<MIXED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem<MIXED>) != cudaSuccess)
+    return 0;
+  sms = sms < kMaxCtas ? sms : kMaxCtas;
+  if (dev < kDevices) ctas[dev].store(sms, std::memory_order_relaxed);
+  return sms;
 }
 
 template <bool MIXED>
 cudaError_t launch_chunk(const ChunkArgs& C, const ChunkMaps& M, cudaStream_t s) {
-  const int ctas = chunk_ctas();
+  const int ctas = chunk_ctas<MIXED>();
   if (ctas < 1) return cudaErrorUnknown;
-  cudaError_t e = cudaFuncSetAttribute(k_chunk<MIXED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem<MIXED>);
-  if (e != cudaSuccess) return e;
   k_chunk<MIXED><<<ctas, kChunkThreads<MIXED>, kChunkSmem<MIXED>, s>>>(C, M);
-  e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
   k_chunk_join<<<dim3(ctas, C.rows / kJoinRows), 256, 0, s>>>(C);
   return cudaGetLastError();

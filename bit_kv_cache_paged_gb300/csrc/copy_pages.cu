@@ -18,15 +18,19 @@ constexpr int kCopyUnroll = 4;                                     // 16-byte lo
 constexpr int kCopyBytes = kCopyThreads * kCopyUnroll * 16;        // 16 KB of one page per CTA
 constexpr int kBf16PageBytes = kPage * kHeadDim * 2;
 static_assert(kBf16PageBytes % kCopyBytes == 0, "a CTA copies whole pieces of a page");
-constexpr int kMaxMoves = 1024;                                    // pairs per launch (8 KB of parameters)
+// Pairs per launch: 8 KB of parameters, or 512 bytes for the few pairs of a fork, whose launch is
+// cheaper on the host.
+constexpr int kMaxMoves = 1024, kFewMoves = 64;
 
+template <int N>
 struct PageMoves {
-  int32_t src[kMaxMoves], dst[kMaxMoves];
+  int32_t src[N], dst[N];
 };
 
 // blockIdx.x: (pair, piece of the page); y: layer; z: K or V
+template <int N>
 __global__ void __launch_bounds__(kCopyThreads) k_copy_pages(uint8_t* k, uint8_t* v, size_t layer_stride, int hkv,
-                                                            const __grid_constant__ PageMoves M) {
+                                                            const __grid_constant__ PageMoves<N> M) {
   const int m = blockIdx.x / hkv, piece = blockIdx.x - m * hkv;
   uint8_t* base = (blockIdx.z ? v : k) + (size_t)blockIdx.y * layer_stride;
   const size_t page = (size_t)hkv * kBf16PageBytes, off = (size_t)piece * kCopyBytes + threadIdx.x * 16;
@@ -37,6 +41,17 @@ __global__ void __launch_bounds__(kCopyThreads) k_copy_pages(uint8_t* k, uint8_t
   for (int i = 0; i < kCopyUnroll; ++i) r[i] = __ldcs(reinterpret_cast<const uint4*>(s + i * kCopyThreads * 16));
 #pragma unroll
   for (int i = 0; i < kCopyUnroll; ++i) *reinterpret_cast<uint4*>(d + i * kCopyThreads * 16) = r[i];
+}
+
+template <int N>
+cudaError_t launch_copy(uint8_t* k, uint8_t* v, size_t layer_stride, int hkv, int n_layers, const int32_t* src, const int32_t* dst,
+                        int32_t m, cudaStream_t st) {
+  PageMoves<N> M;
+  std::copy(src, src + m, M.src);
+  std::copy(dst, dst + m, M.dst);
+  const dim3 grid((unsigned)m * (unsigned)hkv, n_layers, 2);
+  k_copy_pages<N><<<grid, kCopyThreads, 0, st>>>(k, v, layer_stride, hkv, M);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -70,14 +85,11 @@ extern "C" oscar_status oscar_bf16_copy_pages(int32_t num_kv_heads, int32_t n_la
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int32_t per = std::min<int64_t>(kMaxMoves, std::max<int64_t>(1, INT32_MAX / num_kv_heads));
   for (int32_t at = 0; at < n; at += per) {
-    PageMoves M;
     const int32_t m = std::min(per, n - at);
-    std::copy(src + at, src + at + m, M.src);
-    std::copy(dst + at, dst + at + m, M.dst);
-    const dim3 grid((unsigned)m * (unsigned)num_kv_heads, n_layers, 2);
-    k_copy_pages<<<grid, kCopyThreads, 0, st>>>(static_cast<uint8_t*>(k_pages), static_cast<uint8_t*>(v_pages), layer_stride,
-                                               num_kv_heads, M);
-    if (cudaGetLastError() != cudaSuccess) return OSCAR_ECUDA;
+    uint8_t *k = static_cast<uint8_t*>(k_pages), *v = static_cast<uint8_t*>(v_pages);
+    const cudaError_t e = m <= kFewMoves ? launch_copy<kFewMoves>(k, v, layer_stride, num_kv_heads, n_layers, src + at, dst + at, m, st)
+                                         : launch_copy<kMaxMoves>(k, v, layer_stride, num_kv_heads, n_layers, src + at, dst + at, m, st);
+    if (e != cudaSuccess) return OSCAR_ECUDA;
   }
   return OSCAR_OK;
 }

@@ -13,7 +13,18 @@ def _stream():
     return torch.cuda.current_stream().cuda_stream
 
 
+def _raw_stream():
+    """_stream() without making a Stream object, for calls whose kernels take a few microseconds."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _on_current_device(t):
+    return t.is_cuda and t.device.index == torch._C._cuda_getDevice()
+
+
 def _need(t, dtype, shape, name):
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -141,12 +152,15 @@ class Pool:
         _need(k_new, torch.bfloat16, (T, self.Hkv, HEAD_DIM), "k_new")
         _need(v_new, torch.bfloat16, (T, self.Hkv, HEAD_DIM), "v_new")
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        _need(out, torch.bfloat16, q.shape, "out")
+            out = torch.empty_like(q)
+        else:
+            _need(out, torch.bfloat16, (T, self.Hq, HEAD_DIM), "out")
         # a buffer of the call's own: torch's allocator keeps it apart from calls on other streams
         # and from captured graphs
-        workspace = torch.empty(max(B.oscar_chunk_workspace_bytes(self.handle), 16), dtype=torch.uint8, device=q.device)
-        B.oscar_chunk_attend(self.handle, layer, q, k_new, v_new, workspace, out, _stream())
+        lib = B.lib()
+        workspace = torch.empty(max(lib.oscar_chunk_workspace_bytes(self.handle), 16), dtype=torch.uint8, device=q.device)
+        B._check("oscar_chunk_attend", lib.oscar_chunk_attend(self.handle, layer, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+                                                              workspace.data_ptr(), out.data_ptr(), _raw_stream()))
         return out
 
     def step_graph(self, k_new, v_new, q, q_rot=None, out=None):
