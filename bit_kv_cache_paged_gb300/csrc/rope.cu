@@ -8,7 +8,7 @@
 //
 // The work is one read and one write of every row; memory bounds it. A CTA takes one token: its
 // first rot_dim/2 threads make the token's cos and sin once for all heads (shared memory), each
-// thread having its first 16-byte loads of the rows in flight meanwhile.
+// thread having the 16-byte loads of up to four rows in flight meanwhile.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -18,7 +18,8 @@
 namespace oscar {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256;  // at most; kRopeRows head rows of 8 threads each are in flight per thread
+constexpr int kRopeRows = 4;
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
 struct RopeRows {
@@ -78,66 +79,68 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ o
     const int h = i >> 3;
     return h < Q.heads ? xq + h * kHeadDim : xk + (h - Q.heads) * kHeadDim;
   };
-  int i = threadIdx.x;
-  uint4 a = make_uint4(0, 0, 0, 0), b = a;
-  if (i < items) {
-    const uint4* p = reinterpret_cast<const uint4*>(src(i));
-    a = p[c0];
-    b = p[c1];
-  }
-  if (threadIdx.x < half) {
-    const uint64_t turn = (uint64_t)(int64_t)positions[tok] * R.turns[threadIdx.x];
-    float s, co;
-    sincospif((float)(int32_t)(uint32_t)(turn >> 32) * 4.656612873077392578125e-10f, &s, &co);  // 2^-31 of half a turn
-    cs[threadIdx.x] = make_float2(R.amplitude * co, R.amplitude * s);
-  }
-  __syncthreads();
-  for (; i < items;) {
-    const int h = i >> 3;
-    __nv_bfloat16* y = h < Q.heads ? yq + h * kHeadDim : yk + (h - Q.heads) * kHeadDim;
-    uint4 ya = a, yb = b;
-    float fa[8], fb[8];
-    unpack8(a, fa);
-    unpack8(b, fb);
-    // the next row's loads before this row's arithmetic (in place is safe: rows are disjoint)
-    i += kRopeThreads;
-    if (i < items) {
-      const uint4* p = reinterpret_cast<const uint4*>(src(i));
-      a = p[c0];
-      b = p[c1];
-    }
-    if (INTER) {
-      auto spin = [&](float (&f)[8], int chunk) {
+  const int step = blockDim.x;
+  for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < items; i0 += kRopeRows * step) {
+    uint4 a[kRopeRows], b[kRopeRows];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 t = cs[chunk * 4 + e];
-          const float u = f[2 * e], v = f[2 * e + 1];
-          f[2 * e] = u * t.x - v * t.y;
-          f[2 * e + 1] = v * t.x + u * t.y;
+    for (int r = 0; r < kRopeRows; ++r) {
+      if (i0 + r * step < items) {
+        const uint4* p = reinterpret_cast<const uint4*>(src(i0 + r * step));
+        a[r] = p[c0];
+        b[r] = p[c1];
+      }
+    }
+    if (i0 == threadIdx.x) {  // the first time round
+      if (threadIdx.x < half) {
+        const uint64_t turn = (uint64_t)(int64_t)positions[tok] * R.turns[threadIdx.x];
+        float s, co;
+        sincospif((float)(int32_t)(uint32_t)(turn >> 32) * 4.656612873077392578125e-10f, &s, &co);  // 2^-31 of half a turn
+        cs[threadIdx.x] = make_float2(R.amplitude * co, R.amplitude * s);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < kRopeRows; ++r) {
+      const int i = i0 + r * step;
+      if (i >= items) break;
+      const int h = i >> 3;
+      __nv_bfloat16* y = h < Q.heads ? yq + h * kHeadDim : yk + (h - Q.heads) * kHeadDim;
+      float fa[8], fb[8];
+      unpack8(a[r], fa);
+      unpack8(b[r], fb);
+      if (INTER) {
+        auto spin = [&](float (&f)[8], int chunk) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 t = cs[chunk * 4 + e];
+            const float u = f[2 * e], v = f[2 * e + 1];
+            f[2 * e] = u * t.x - v * t.y;
+            f[2 * e + 1] = v * t.x + u * t.y;
+          }
+        };
+        if (turn0) {
+          spin(fa, c0);
+          a[r] = pack8(fa);
         }
-      };
-      if (turn0) {
-        spin(fa, c0);
-        ya = pack8(fa);
-      }
-      if (turn1) {
-        spin(fb, c1);
-        yb = pack8(fb);
-      }
-    } else if (turn0) {
+        if (turn1) {
+          spin(fb, c1);
+          b[r] = pack8(fb);
+        }
+      } else if (turn0) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 t = cs[c0 * 8 + e];
-        const float u = fa[e], v = fb[e];
-        fa[e] = u * t.x - v * t.y;
-        fb[e] = v * t.x + u * t.y;
+        for (int e = 0; e < 8; ++e) {
+          const float2 t = cs[c0 * 8 + e];
+          const float u = fa[e], v = fb[e];
+          fa[e] = u * t.x - v * t.y;
+          fb[e] = v * t.x + u * t.y;
+        }
+        a[r] = pack8(fa);
+        b[r] = pack8(fb);
       }
-      ya = pack8(fa);
-      yb = pack8(fb);
+      uint4* o = reinterpret_cast<uint4*>(y);
+      o[c0] = a[r];
+      o[c1] = b[r];
     }
-    uint4* o = reinterpret_cast<uint4*>(y);
-    o[c0] = ya;
-    o[c1] = yb;
   }
 }
 
@@ -218,10 +221,13 @@ oscar_status oscar_rope_apply(const oscar_rope* rope, int32_t n, const int32_t* 
   const RopeRows Q{static_cast<const __nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(q_out), qs, qos, num_q_heads};
   const RopeRows K{static_cast<const __nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(k_out), ks, kos, num_k_heads};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // threads that divide the token's rows evenly, at least one per pair
+  const int64_t items = 8 * ((int64_t)num_q_heads + num_k_heads), rounds = (items + kRopeThreads - 1) / kRopeThreads;
+  const int threads = (int)std::max<int64_t>(64, ((items + rounds - 1) / rounds + 31) / 32 * 32);
   if (rope->interleaved)
-    k_rope<true><<<n, kRopeThreads, 0, st>>>(*rope, Q, K, positions);
+    k_rope<true><<<n, threads, 0, st>>>(*rope, Q, K, positions);
   else
-    k_rope<false><<<n, kRopeThreads, 0, st>>>(*rope, Q, K, positions);
+    k_rope<false><<<n, threads, 0, st>>>(*rope, Q, K, positions);
   if (cudaGetLastError() != cudaSuccess) return OSCAR_ECUDA;
   return OSCAR_OK;
 }
