@@ -78,7 +78,7 @@ struct ChunkArgs {
   int64_t n_pages_total;
   // pool
   DevPool P;
-  int32_t layer;
+  int32_t layer, skip_single;
   const __nv_bfloat16* v_new;
   __nv_bfloat16* out;
   uint8_t* ws;
@@ -110,6 +110,7 @@ __device__ __forceinline__ SeqWork load_seq(const ChunkArgs& C, int i) {
   if constexpr (MIXED) {
     const StepSeq& st = C.P.step[i];
     s.n = st.L_new - st.L_old;
+    if (C.skip_single && s.n == 1) s.n = 0;
     s.row0 = st.in_offset;
     s.F = st.F_old;
     s.L = st.L_old;
@@ -1527,8 +1528,8 @@ size_t chunk_workspace_bytes(int hg, int64_t n_tokens) {
   return 32 + (size_t)kMaxCtas * (kDescBytes + 2 * (size_t)slot_rows(hg, n_tokens) * (kHeadDim + 2) * 4);
 }
 
-cudaError_t launch_chunk_pool(const DevPool& P, const StepDims& S, int layer, const void* q, const void* k_new,
-                              const void* v_new, void* workspace, void* out, cudaStream_t s) {
+cudaError_t launch_chunk_pool(const DevPool& P, const StepDims& S, int layer, bool skip_single, const void* q,
+                              const void* k_new, const void* v_new, void* workspace, void* out, cudaStream_t s) {
   ChunkArgs C{};
   C.Hq = P.Hq;
   C.Hkv = P.Hkv;
@@ -1538,6 +1539,7 @@ cudaError_t launch_chunk_pool(const DevPool& P, const StepDims& S, int layer, co
   C.rows = slot_rows(P.hg, S.total_new);
   C.P = P;
   C.layer = layer;
+  C.skip_single = skip_single;
   C.v_new = static_cast<const __nv_bfloat16*>(v_new);
   set_buffers(C, workspace, out);
   C.err = P.err;

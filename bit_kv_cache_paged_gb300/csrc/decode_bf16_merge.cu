@@ -357,15 +357,31 @@ __device__ __forceinline__ void combine_slots(int n, SlotFn slot, int hh, int la
   }
 }
 
+// Rows of new tokens: q [n_seqs][Hq][128] by batch index; k, v and out by in_offset.
+struct NewRows {
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16* out;
+};
+
+__device__ __forceinline__ void load_bf16x4(const __nv_bfloat16* p, float (&x)[4]) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  x[0] = __uint_as_float(w.x << 16);
+  x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+  x[2] = __uint_as_float(w.y << 16);
+  x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+}
+
 // One CTA per (group of rows, KV head), a row being one (sequence, query head): WPR warps per row
 // (kRowWarps / WPR rows per CTA). The warps of a row each softmax-combine every WPR-th INT2 split
 // (rotated basis) and the first one joins their results through shared memory; then the
 // un-rotation by U_V^T staged in shared memory, and the merge with the BF16 partial. Two warps
-// per row serve steps with many splits per row (few sequences), one warp the others.
-template <int HG, int WPR>
+// per row serve steps with many splits per row (few sequences), one warp the others. NEW: the row's own
+// new token joins as one more key (its score from q, k_new and v_new rows at the sequence's in_offset),
+// and the output goes to that row in bf16.
+template <int HG, int WPR, bool NEW>
 __global__ void __launch_bounds__(kRowWarps * 32)
     k_merge(DevPool P, StepDims S, int layer, const float* __restrict__ pint2, const float* __restrict__ pbf16,
-            float* __restrict__ out) {
+            float* __restrict__ out, NewRows N) {
   static_assert(kRowsPerWarp == 1, "one row per warp");
   constexpr int RPC = kRowWarps / WPR;  // rows per CTA
   constexpr int SLOT = HG * (2 + kHeadDim);
@@ -459,6 +475,30 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     return pbf16 + ((size_t)pair * kBfSlotsPerPair + k) * SLOT;
   }, hh, lane, Mb, Lb, ab);
   float res[4] = {0.f, 0.f, 0.f, 0.f};
+  if constexpr (NEW) {
+    const int64_t at = P.step[bi].in_offset, kvo = (at * P.Hkv + h) * kHeadDim + 4 * lane;
+    float q4[4], k4[4], v4[4];
+    load_bf16x4(N.q + ((int64_t)bi * P.Hq + (int64_t)h * HG + hh) * kHeadDim + 4 * lane, q4);
+    load_bf16x4(N.k + kvo, k4);
+    load_bf16x4(N.v + kvo, v4);
+    float d = q4[0] * k4[0] + q4[1] * k4[1] + q4[2] * k4[2] + q4[3] * k4[3];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    d *= kScoreLog2;
+    const float Mx = fmaxf(fmaxf(Mi, Mb), d);
+    if (Mx > -INFINITY || d != d) {
+      const float wi = (Li > 0.f) ? Li * fast_exp2(Mi - Mx) : 0.f;
+      const float eb = (Lb > 0.f) ? fast_exp2(Mb - Mx) : 0.f;
+      const float en = fast_exp2(d - Mx);
+      const float den = wi + Lb * eb + en;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) res[e] = (wi * oi[0][e] + eb * ab[e] + en * v4[e]) / den;
+    }
+    const __nv_bfloat162 x = __floats2bfloat162_rn(res[0], res[1]), y = __floats2bfloat162_rn(res[2], res[3]);
+    *reinterpret_cast<uint2*>(N.out + (at * P.Hq + (int64_t)h * HG + hh) * kHeadDim + 4 * lane) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    return;
+  }
   const float Mx = fmaxf(Mi, Mb);
   if (Mx > -INFINITY) {
     const float wi = (Li > 0.f) ? Li * fast_exp2(Mi - Mx) : 0.f;
@@ -480,8 +520,8 @@ inline int merge_wpr(const StepDims& S) { return S.nw_max >= 16 * S.n_pairs ? 2 
 cudaError_t preload_decode_bf16_merge(int hg) {
   cudaFuncAttributes a;
   cudaError_t e = hg == 4 ? cudaFuncGetAttributes(&a, k_decode_bf16<4>) : cudaFuncGetAttributes(&a, k_decode_bf16<8>);
-  if (e == cudaSuccess) e = hg == 4 ? cudaFuncGetAttributes(&a, k_merge<4, 1>) : cudaFuncGetAttributes(&a, k_merge<8, 1>);
-  if (e == cudaSuccess) e = hg == 4 ? cudaFuncGetAttributes(&a, k_merge<4, 2>) : cudaFuncGetAttributes(&a, k_merge<8, 2>);
+  if (e == cudaSuccess) e = hg == 4 ? cudaFuncGetAttributes(&a, k_merge<4, 1, false>) : cudaFuncGetAttributes(&a, k_merge<8, 1, false>);
+  if (e == cudaSuccess) e = hg == 4 ? cudaFuncGetAttributes(&a, k_merge<4, 2, false>) : cudaFuncGetAttributes(&a, k_merge<8, 2, false>);
   return e;
 }
 
@@ -515,24 +555,40 @@ cudaError_t launch_rotate_q(const DevPool& P, const StepDims& S, int layer, cons
   return cudaGetLastError();
 }
 
-cudaError_t launch_merge(const DevPool& P, const StepDims& S, int layer, const float* partials_int2,
-                         const float* partials_bf16, float* out, cudaStream_t s) {
+namespace {
+template <bool NEW>
+cudaError_t launch_merge_t(const DevPool& P, const StepDims& S, int layer, const float* partials_int2,
+                           const float* partials_bf16, float* out, const NewRows& N, cudaStream_t s) {
   if (S.n_pairs <= 0) return cudaSuccess;
   const int wpr = merge_wpr(S), rpc = kRowWarps / wpr;
   dim3 grid((S.n_seqs * P.hg + rpc - 1) / rpc, P.Hkv);
   const int smem = kUBytes + 16 + kRowWarps * kHeadDim * 4 + (wpr > 1 ? kRowWarps * (2 + kHeadDim) * 4 : 0);
   auto go = [&](auto kernel) {
     cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    kernel<<<grid, kRowWarps * 32, smem, s>>>(P, S, layer, partials_int2, partials_bf16, out);
+    kernel<<<grid, kRowWarps * 32, smem, s>>>(P, S, layer, partials_int2, partials_bf16, out, N);
   };
   if (P.hg == 4) {
-    if (wpr > 1) go(k_merge<4, 2>);
-    else go(k_merge<4, 1>);
+    if (wpr > 1) go(k_merge<4, 2, NEW>);
+    else go(k_merge<4, 1, NEW>);
   } else {
-    if (wpr > 1) go(k_merge<8, 2>);
-    else go(k_merge<8, 1>);
+    if (wpr > 1) go(k_merge<8, 2, NEW>);
+    else go(k_merge<8, 1, NEW>);
   }
   return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_merge(const DevPool& P, const StepDims& S, int layer, const float* partials_int2,
+                         const float* partials_bf16, float* out, cudaStream_t s) {
+  return launch_merge_t<false>(P, S, layer, partials_int2, partials_bf16, out, NewRows{}, s);
+}
+
+cudaError_t launch_merge_new(const DevPool& P, const StepDims& S, int layer, const float* partials_int2,
+                             const float* partials_bf16, const void* q, const void* k_new, const void* v_new, void* out,
+                             cudaStream_t s) {
+  const NewRows N{static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k_new),
+                  static_cast<const __nv_bfloat16*>(v_new), static_cast<__nv_bfloat16*>(out)};
+  return launch_merge_t<true>(P, S, layer, partials_int2, partials_bf16, nullptr, N, s);
 }
 
 }  // namespace oscar

@@ -121,10 +121,32 @@ cudaError_t launch_decode_bf16(const DevPool& P, const StepDims& S, int layer, c
                                float* partials, cudaStream_t s);
 cudaError_t launch_merge(const DevPool& P, const StepDims& S, int layer, const float* partials_int2,
                          const float* partials_bf16, float* out, cudaStream_t s);
+// launch_merge with each row's own new token as one more key, output in bf16 (chunk_single.cu).
+cudaError_t launch_merge_new(const DevPool& P, const StepDims& S, int layer, const float* partials_int2,
+                             const float* partials_bf16, const void* q, const void* k_new, const void* v_new, void* out,
+                             cudaStream_t s);
+
 // Attention of new tokens over a cache (chunk.cu). workspace: chunk_workspace_bytes() bytes.
+// skip_single: leave out the sequences of one new token.
 size_t chunk_workspace_bytes(int hg, int64_t n_tokens);
-cudaError_t launch_chunk_pool(const DevPool& P, const StepDims& S, int layer, const void* q, const void* k_new,
-                              const void* v_new, void* workspace, void* out, cudaStream_t s);
+cudaError_t launch_chunk_pool(const DevPool& P, const StepDims& S, int layer, bool skip_single, const void* q,
+                              const void* k_new, const void* v_new, void* workspace, void* out, cudaStream_t s);
+// The sequences of one new token by the decode kernels (chunk_single.cu). S1: their batch before the
+// step (n_seqs, n_pairs, total_units, nw_max and nw of it).
+size_t chunk_single_workspace_bytes(const DevPool& P, const StepDims& S1);
+cudaError_t launch_chunk_single(const DevPool& P, const StepDims& S, const StepDims& S1, int layer,
+                                const void* q, const void* k_new, const void* v_new, void* workspace, void* out,
+                                cudaStream_t s, int* launches);
+// INT2 decode workers (see step_begin)
+constexpr int kMaxPartialsPerPair = 64;  // per (sequence, KV head), on average, at most: bounds the merge's work
+__host__ __device__ inline int int2_workers(int64_t units, int64_t n_pairs, int64_t max_workers) {
+  if (units <= 0) return 0;
+  // at least kMinUnitsPerWorker pages per worker, and at most kMaxPartialsPerPair partials per pair
+  int64_t want = (units + kMinUnitsPerWorker - 1) / kMinUnitsPerWorker;
+  want = want < n_pairs * kMaxPartialsPerPair ? want : n_pairs * kMaxPartialsPerPair;
+  want = want < max_workers ? want : max_workers;
+  return (int)(want > 1 ? want : 1);
+}
 cudaError_t launch_debug_rotate(const DevPool& P, int layer, int head, int kv, const void* x, int n,
                                 float* out, cudaStream_t s);
 cudaError_t launch_debug_read_int2(const DevPool& P, int seq, int layer, int head, int pos0, int n,

@@ -152,8 +152,11 @@ struct oscar_pool {
 
 namespace {
 
-// INT2 decode workers per (sequence, KV head), on average, at most: bounds the merge's work
-constexpr int kMaxPartialsPerPair = 64;
+// Single new tokens go to the decode kernels (five short launches) when their histories have this many
+// INT2 pages (of one KV head) per SM. Measured with 8 KV heads, 4 query heads each, group 128, chunk
+// kernel against decode kernels: 3.1 pages 27.4 and 27.8 us, 4.6 pages 35.3 and 30.7 us, 24 pages 51.3
+// and 32.5 us.
+constexpr int64_t kSingleMinPagesPerSm = 4;
 
 oscar_status cuda_fail(cudaError_t e) {
   if (e == cudaSuccess) return OSCAR_OK;
@@ -567,15 +570,7 @@ oscar_status oscar_step_begin(oscar_pool* p, const int32_t* seq_ids, const int32
   D.total_units = (int32_t)tot_units;
   D.n_pairs = n_seqs * Hkv;
   D.nw_max = (int32_t)std::max<int64_t>(1, std::min<int64_t>(p->max_workers, (int64_t)n_seqs * Hkv * kMaxPartialsPerPair));
-  if (tot_units > 0) {
-    // at least kMinUnitsPerWorker pages per worker, and at most kMaxPartialsPerPair partials per
-    // (sequence, KV head) on average, which bounds the merge's work when a step has few rows
-    const int64_t want = std::min<int64_t>((tot_units + kMinUnitsPerWorker - 1) / kMinUnitsPerWorker,
-                                           (int64_t)n_seqs * Hkv * kMaxPartialsPerPair);
-    D.nw = (int32_t)std::max<int64_t>(1, std::min<int64_t>(p->max_workers, want));
-  } else {
-    D.nw = 0;
-  }
+  D.nw = int2_workers(tot_units, (int64_t)n_seqs * Hkv, p->max_workers);
   p->in_step = true;
   p->stepped = true;
   std::fill(p->appended.begin(), p->appended.end(), (uint8_t)0);
@@ -636,9 +631,40 @@ oscar_status oscar_rotate_q(oscar_pool* p, int32_t layer, const void* q, float* 
   return timed_launch(p, OSCAR_KERNEL_ROTATE_Q, st, [&] { return launch_rotate_q(p->P, p->dims, layer, q, q_rot, st); });
 }
 
+// How a step's new tokens are attended: sequences of one new token by the decode kernels when their
+// histories are long, the others (or all) by the chunk kernel.
+struct ChunkPlan {
+  StepDims single;  // the single-token sequences' batch, before the step (n_seqs 0: none apart)
+  bool chunk;       // rows for the chunk kernel
+  size_t chunk_bytes, single_bytes;
+};
+
+static ChunkPlan chunk_plan(const oscar_pool* p) {
+  ChunkPlan c{};
+  int64_t n1 = 0, units = 0;
+  for (const StepSeq& s : p->step) {
+    if (s.L_new - s.L_old != 1) continue;
+    ++n1;
+    units += (int64_t)p->cfg.num_kv_heads * pages_for(s.F_old);
+  }
+  if (units >= kSingleMinPagesPerSm * (int64_t)p->num_sms) {
+    StepDims& d = c.single;
+    d.n_seqs = (int32_t)n1;
+    d.n_pairs = (int32_t)(n1 * p->cfg.num_kv_heads);
+    d.total_units = (int32_t)units;
+    d.nw_max = (int32_t)std::max<int64_t>(1, std::min<int64_t>(p->max_workers, (int64_t)d.n_pairs * kMaxPartialsPerPair));
+    d.nw = int2_workers(units, d.n_pairs, p->max_workers);
+    c.single_bytes = chunk_single_workspace_bytes(p->P, d);
+  }
+  c.chunk = p->dims.total_new > c.single.n_seqs;
+  c.chunk_bytes = c.chunk ? align_up(chunk_workspace_bytes(p->hg, p->dims.total_new)) : 0;
+  return c;
+}
+
 size_t oscar_chunk_workspace_bytes(const oscar_pool* p) {
   if (!p || !p->in_step || p->host_only) return 0;
-  return chunk_workspace_bytes(p->hg, p->dims.total_new);
+  const ChunkPlan c = chunk_plan(p);
+  return c.chunk_bytes + c.single_bytes + kAlign;
 }
 
 oscar_status oscar_chunk_attend(oscar_pool* p, int32_t layer, const void* q, const void* k_new, const void* v_new,
@@ -653,10 +679,20 @@ oscar_status oscar_chunk_attend(oscar_pool* p, int32_t layer, const void* q, con
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return cuda_fail(cudaErrorUnknown);
   if (dev != p->device) return OSCAR_EINVAL;
-  const cudaError_t e = launch_chunk_pool(p->P, p->dims, layer, q, k_new, v_new, workspace, out, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e);
-  p->launch_count++;
-  return OSCAR_OK;
+  const ChunkPlan c = chunk_plan(p);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<uintptr_t>(workspace)));
+  cudaError_t e = cudaSuccess;
+  if (c.single.n_seqs > 0) {
+    int n = 0;
+    e = launch_chunk_single(p->P, p->dims, c.single, layer, q, k_new, v_new, ws + c.chunk_bytes, out, st, &n);
+    p->launch_count += n;
+  }
+  if (e == cudaSuccess && c.chunk) {
+    e = launch_chunk_pool(p->P, p->dims, layer, c.single.n_seqs > 0, q, k_new, v_new, ws, out, st);
+    p->launch_count += 2;
+  }
+  return cuda_fail(e);
 }
 
 size_t oscar_partials_bytes(const oscar_pool* p, int32_t n_seqs) {

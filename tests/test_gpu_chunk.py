@@ -341,6 +341,54 @@ def test_pool_ragged_chunks(group, absorbed, lloyd, hq):
     m.chunk([10, 0, 4], [0, 260, 129])
 
 
+@pytest.mark.parametrize("group,absorbed,lloyd,hq", [(128, False, None, 32), (32, False, None, 64), (128, True, None, 64), (32, True, (1.2, 0.8), 32),
+                                                     (128, False, (0.9, 1.3), 64)])
+def test_pool_single_tokens_over_long_histories(group, absorbed, lloyd, hq):
+    """Single tokens whose histories together are long take another path than chunks; alone, and beside chunks."""
+    m = Mixed(hq=hq, hkv=8, group=group, absorbed=absorbed, lloyd=lloyd, seed=group + hq, max_seqs=8, max_len=4096)
+    ctx = [3500, 0, 400, 3904, 63, 2000, 1000, 330]
+    ids = list(range(8))
+    for i in ids:
+        m.add(i)
+    m.pool.step_begin(ids, ctx)
+    kv = m.new_rows(sum(ctx))
+    m.pool.append_and_demote(0, kv[0][0], kv[1][0])
+    r = 0
+    for i, n in zip(ids, ctx):
+        m.rows[i] = [x[:, r:r + n] for x in kv]
+        r += n
+    launches = m.pool.launch_count()
+    m.chunk(ids, [1] * 8)
+    assert m.pool.launch_count() - launches > 6  # the decode kernels ran: a chunk is two launches a call
+    m.chunk([3, 5, 1, 0], [1, 7, 1, 1])
+    m.chunk([2, 0, 3, 6], [0, 1, 1, 130])
+
+
+def test_pool_single_tokens_bad_value_and_bad_page():
+    m = Mixed(hq=32, hkv=8, seed=22, max_seqs=4, max_len=4096)
+    for i in range(4):
+        m.add(i)
+    m.pool.step_begin([0, 1, 2, 3], [3500, 3000, 2500, 3800])
+    kv = m.new_rows(12800)
+    m.pool.append_and_demote(0, kv[0][0], kv[1][0])
+    m.pool.step_begin([0, 1, 2, 3], [1, 1, 1, 1])
+    kn, vn = m.new_rows(4)
+    q = torch.randn((4, 32, E), generator=m.g, device="cuda").bfloat16()
+    good = m.pool.chunk_attend(0, q, kn[0], vn[0])
+    vn[0, 1, 0, 9], kn[0, 2, 3, 5] = math.inf, math.nan
+    out = m.pool.chunk_attend(0, q, kn[0], vn[0])
+    assert torch.equal(out[[0, 3]], good[[0, 3]]) and torch.equal(out[1, 4:], good[1, 4:])
+    assert (out[1, :4, 9] == math.inf).all() and out[1, :4, :9].isfinite().all()
+    assert out[2, 12:16].isnan().all() and torch.equal(out[2, :12], good[2, :12])
+    m.pool.check()
+    st = torch.cuda.current_stream().cuda_stream
+    B.oscar_debug_set_page_entry(m.pool.handle, 3, 7, m.pool.cfg.max_int2_pages, st)
+    out = m.pool.chunk_attend(0, q, kn[0], vn[0])
+    with pytest.raises(B.OscarError) as e:
+        m.pool.check()
+    assert e.value.detail & B.DEVERR_PAGE and torch.equal(out[0], good[0])
+
+
 def test_pool_first_prefill_and_decode_afterwards():
     """rotary positions, chunks from the first token on, and a decode step at the end, as a server runs them."""
     m = Mixed(hq=8, hkv=2, seed=3)
