@@ -15,8 +15,8 @@ BUILD = os.path.join(ROOT, "_build", platform.machine(), "oscar")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "liboscar.so")
 SOURCES = ["pool.cpp", "demote.cu", "decode_int2.cu", "decode_bf16_merge.cu", "decode_noalloc.cu", "bf16_baseline.cu", "demote_tc.cu",
-           "chunk.cu", "chunk_single.cu", "rope.cu", "copy_pages.cu"]
-HEADERS = ["oscar_internal.h", "device_common.cuh", "tcgen05.cuh"]
+           "chunk.cu", "chunk_single.cu", "chunk_tiles.cu", "rope.cu", "copy_pages.cu"]
+HEADERS = ["oscar_internal.h", "device_common.cuh", "tcgen05.cuh", "int2_tiles.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -37,16 +37,21 @@
 #include <cstring>
 #include <type_traits>
 
+#include "int2_tiles.cuh"
 #include "tcgen05.cuh"
 
 namespace oscar {
 namespace {
 
+// The BF16-only cache; the pool with INT2 blocks dequantised in the kernel; the pool with their fp16
+// tiles made beforehand.
+enum { kBf16 = 0, kDequant = 1, kTiles = 2 };
+
 constexpr int kTile = 128;                    // rows of a tile, keys of a block
 constexpr int kHalfBytes = kTile * 128;       // 64 dims of 128 rows
 constexpr int kTileBytes = 2 * kHalfBytes;    // 128 x 128 16-bit values
-template <bool MIXED>
-constexpr int kStages = MIXED ? 4 : 5;        // K / V tiles in flight
+template <int MODE>
+constexpr int kStages = MODE == kDequant ? 4 : 5;  // K / V tiles in flight
 constexpr int kCodeBuf = 3 * 2 * int2_block_bytes(128);  // packed INT2 pages in flight: three blocks (two of groups of 32)
 constexpr int kMaxSlots = 3;
 constexpr int kMaxCtas = 152;
@@ -80,6 +85,9 @@ struct ChunkArgs {
   DevPool P;
   int32_t layer, skip_single;
   const __nv_bfloat16* v_new;
+  // the history's fp16 tiles (mode kTiles): of sequence i from block tile_base[i] on, [KV head][block][K, V]
+  const uint8_t* tiles;
+  const int32_t* tile_base;
   __nv_bfloat16* out;
   uint8_t* ws;
   uint32_t* err;
@@ -102,12 +110,13 @@ struct SeqWork {
   int32_t n, A, row0;
   int32_t nI, nB;                 // INT2 blocks, blocks of cached BF16 pages (pool)
   int32_t hist, F, L, sink, seq;  // pool: history tokens, frontier and length before the step
+  int32_t tile0;                  // first block of its tiles
 };
 
-template <bool MIXED>
+template <int MODE>
 __device__ __forceinline__ SeqWork load_seq(const ChunkArgs& C, int i) {
   SeqWork s{};
-  if constexpr (MIXED) {
+  if constexpr (MODE != kBf16) {
     const StepSeq& st = C.P.step[i];
     s.n = st.L_new - st.L_old;
     if (C.skip_single && s.n == 1) s.n = 0;
@@ -122,6 +131,7 @@ __device__ __forceinline__ SeqWork load_seq(const ChunkArgs& C, int i) {
     const int ring = s.L > s.F ? ((s.L - 1) >> 6) - (s.F >> 6) + 1 : 0;
     s.nB = s.L > 0 ? (1 + ring + 1) / 2 : 0;
     s.A = 0;
+    if (MODE == kTiles) s.tile0 = C.tile_base[i];
   } else {
     const int a = min(max(C.cu[i], 0), C.n_tokens), b = min(max(C.cu[i + 1], a), C.n_tokens);
     int len = max(C.lengths[i], 0);
@@ -182,7 +192,7 @@ __device__ __forceinline__ int cut_at(const SeqWork& s, int tiles, int64_t x, in
 
 // A place in the order (sequence, KV head, tile pair, block), moved segment by segment up to the
 // CTA's end.
-template <bool MIXED>
+template <int MODE>
 struct Cursor {
   SeqWork s;
   int i, h, t, k0, k1, nb;  // the segment: blocks [k0, k1) of nb
@@ -195,7 +205,7 @@ struct Cursor {
     h = h_;
     t = t_;
     end = x + n;
-    s = load_seq<MIXED>(C, i);
+    s = load_seq<MODE>(C, i);
     nb = max(1, real_blocks(s, lg, t));
     k0 = cut_at(s, tiles(), x, nb);
     k1 = cut_at(s, tiles(), end, nb);
@@ -212,7 +222,7 @@ struct Cursor {
         h = 0;
         do {
           ++i;
-          s = load_seq<MIXED>(C, i);
+          s = load_seq<MODE>(C, i);
         } while (s.n == 0 && i + 1 < C.n_seqs);
       }
     }
@@ -233,15 +243,15 @@ struct Half {
   int lo, hi;
   int pos;  // BF16 cache: page index; pool: first chunk row, or position of slot 0 in the ring, -1 the sink
 };
-template <bool MIXED>
+template <int MODE>
 __device__ __forceinline__ Half half_of(const SeqWork& s, int k, int half) {
   Half r;
-  if (MIXED && k < s.nI) {
+  if (MODE != kBf16 && k < s.nI) {
     const int j = 2 * k + half;
     r.lo = 0;
     r.hi = min(max(s.hist - j * kPage, 0), kPage);
     r.pos = j;
-  } else if (MIXED && k < s.nI + s.nB) {
+  } else if (MODE != kBf16 && k < s.nI + s.nB) {
     const int j = 2 * (k - s.nI) + half;
     if (j == 0) {
       r.lo = 0;
@@ -273,9 +283,9 @@ struct Clean {
   int32_t stage, slot;  // slot: row of `bad` that takes the keys found; stage -1: no more
 };
 
-template <bool MIXED>
+template <int MODE>
 struct Shared {
-  uint64_t full[kStages<MIXED>], empty[kStages<MIXED>], code_full[kMaxSlots], code_empty[kMaxSlots];
+  uint64_t full[kStages<MODE>], empty[kStages<MODE>], code_full[kMaxSlots], code_empty[kMaxSlots];
   // S of a block is followed by its P, so s_full never runs ahead of the rows' threads; O has a barrier of
   // its own, since nothing answers it before the next S
   uint64_t q_full, q_empty, s_full[2], p_ready[2], o_full[2], done, clean_go, clean_done;
@@ -288,13 +298,13 @@ struct Shared {
   // non-finite values of the diagonal blocks: key bits per block, two segments in turn
   uint32_t bad[2][4][4];
   uint32_t any_bad[2];
-  Cursor<MIXED> cursors[8];  // of the softmax warps, whose registers hold scores
+  Cursor<MODE> cursors[8];  // of the softmax warps, whose registers hold scores
 };
 constexpr int kSharedBytes = 2048;
-static_assert(sizeof(Shared<true>) <= kSharedBytes && sizeof(Shared<false>) <= kSharedBytes, "Shared");
-template <bool MIXED>
-constexpr int kChunkSmem = (2 + kStages<MIXED>) * kTileBytes + (MIXED ? kCodeBuf : 0) + kSharedBytes;
-static_assert(kChunkSmem<true> <= 232448 && kChunkSmem<false> <= 232448, "shared memory of an SM");
+static_assert(sizeof(Shared<kDequant>) <= kSharedBytes && sizeof(Shared<kBf16>) <= kSharedBytes, "Shared");
+template <int MODE>
+constexpr int kChunkSmem = (2 + kStages<MODE>) * kTileBytes + (MODE == kDequant ? kCodeBuf : 0) + kSharedBytes;
+static_assert(kChunkSmem<kDequant> <= 232448 && kChunkSmem<kBf16> <= 232448, "shared memory of an SM");
 
 // One try that sleeps up to ns nanoseconds: a spinning warp takes issue slots from the others.
 __device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity, uint32_t ns) {
@@ -307,8 +317,8 @@ __device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity
   return ok != 0;
 }
 // Bounded wait that also ends when another role gave up. SLEEP: for roles with time to spare.
-template <bool SLEEP = false, bool MIXED>
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Shared<MIXED>* sh, uint32_t* err) {
+template <bool SLEEP = false, int MODE>
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Shared<MODE>* sh, uint32_t* err) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
@@ -322,8 +332,8 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Shared<
 }
 // The same for a whole warp, which leaves it converged (tensor-memory instructions and aligned
 // barriers follow).
-template <bool SLEEP = false, bool MIXED>
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Shared<MIXED>* sh, uint32_t* err) {
+template <bool SLEEP = false, int MODE>
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Shared<MODE>* sh, uint32_t* err) {
   const bool ok = wait_bar<SLEEP>(bar, parity, sh, err);
   __syncwarp();
   return __all_sync(0xffffffffu, ok);
@@ -340,17 +350,17 @@ __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
 // both go through every position: a stage is empty again when its tile has been used (one arrival, of
 // the tensor cores) and when the producer it does not belong to has passed it (four arrivals).
 constexpr int kPassers = 4;
-template <bool MIXED>
+template <int MODE>
 struct Ring {  // position in the stream of K / V tiles
   uint32_t pos = 0;
-  __device__ __forceinline__ int stage() const { return pos % kStages<MIXED>; }
-  __device__ __forceinline__ uint32_t parity() const { return (pos / kStages<MIXED>) & 1; }
+  __device__ __forceinline__ int stage() const { return pos % kStages<MODE>; }
+  __device__ __forceinline__ uint32_t parity() const { return (pos / kStages<MODE>) & 1; }
 };
 // A tile's full barrier counts the four dequantising warps; a tensor copy's lane arrives for all.
-template <bool MIXED>
+template <int MODE>
 __device__ __forceinline__ void expect_tile(uint64_t* bar, uint32_t bytes) {
   mbar_expect_tx(bar, bytes);
-  if (MIXED) mbar_arrive_n(bar, 3);
+  if (MODE == kDequant) mbar_arrive_n(bar, 3);
 }
 // Blocks of packed pages that fit the code buffer.
 __device__ __forceinline__ int code_slots(const DevPool& P) { return P.ngroups == 1 ? 3 : 2; }
@@ -359,12 +369,12 @@ __device__ __forceinline__ int code_slots(const DevPool& P) { return P.ngroups =
 constexpr int kLimbs = 2;
 
 // ---- tensor-copy warp --------------------------------------------------------------------------
-template <bool MIXED>
-__device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MIXED>* sh, uint8_t* sq, uint8_t* ring, uint8_t* codes,
-                          Cursor<MIXED> cur) {
+template <int MODE>
+__device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MODE>* sh, uint8_t* sq, uint8_t* ring, uint8_t* codes,
+                          Cursor<MODE> cur) {
   // one lane
   const uint64_t keep = policy_evict_last(), once = policy_evict_first();
-  Ring<MIXED> r;
+  Ring<MODE> r;
   uint32_t issued = 0, qn = 0;  // bit s: stage s has had a tensor copy
   uint32_t last_parity = 0;
   bool ok = true;
@@ -391,6 +401,7 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MIXED>*
   auto skip = [&](int n) {  // tiles that the dequantising warps fill
     for (; n > 0; --n, ++r.pos) {
       if (!wait_bar<true>(&sh->empty[r.stage()], r.parity() ^ 1, sh, C.err)) return false;
+      issued &= ~(1u << r.stage());
       mbar_arrive_n(&sh->empty[r.stage()], 4);
     }
     return true;
@@ -401,8 +412,19 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MIXED>*
       uint8_t* dst;
       uint64_t* bar;
       if (!stage(dst, bar)) return false;
-      expect_tile<MIXED>(bar, kTileBytes);
+      expect_tile<MODE>(bar, kTileBytes);
       bulk_g2s(dst, src + l * kTileBytes, kTileBytes, bar, keep);
+    }
+    return true;
+  };
+  auto load_tiles = [&](int k) {  // the fp16 tiles of INT2 block k
+    const uint8_t* src = C.tiles + ((int64_t)cur.s.tile0 * C.Hkv + (int64_t)cur.h * cur.s.nI + k) * (2 * kTileBytes);
+    for (int kv = 0; kv < 2; ++kv) {
+      uint8_t* dst;
+      uint64_t* bar;
+      if (!stage(dst, bar)) return false;
+      mbar_expect_tx(bar, kTileBytes);
+      bulk_g2s(dst, src + kv * kTileBytes, kTileBytes, bar, keep);
     }
     return true;
   };
@@ -437,8 +459,8 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MIXED>*
     bool rows3 = false;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      hf[x] = half_of<MIXED>(cur.s, k, x);
-      if constexpr (MIXED) {
+      hf[x] = half_of<MODE>(cur.s, k, x);
+      if constexpr (MODE != kBf16) {
         rows3 = k >= cur.s.nI + cur.s.nB;
         if (rows3) {
           row[x] = cur.s.row0 + hf[x].pos * kPage;
@@ -471,14 +493,14 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MIXED>*
       uint8_t* dst;
       uint64_t* bar;
       if (!stage(dst, bar)) return false;
-      expect_tile<MIXED>(bar, n * 2 * kPageHalfBytes);
+      expect_tile<MODE>(bar, n * 2 * kPageHalfBytes);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (hf[x].hi <= hf[x].lo) continue;
 #pragma unroll
         for (int d = 0; d < 2; ++d) {
           uint8_t* to = dst + d * kHalfBytes + x * kPageHalfBytes;
-          if (MIXED && rows3)
+          if (MODE != kBf16 && rows3)
             tma_load_3d(to, map[x][kv], d * 64, cur.h, row[x], bar, keep);
           else
             tma_load_2d(to, map[x][kv], d * 64, row[x], bar, keep);
@@ -489,11 +511,16 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MIXED>*
   };
   for (; ok && cur.valid(); cur.next(C)) {
     if (cur.empty()) continue;
-    const int nI = MIXED ? min(cur.k1, cur.s.nI) : 0;
+    const int nI = MODE != kBf16 ? min(cur.k1, cur.s.nI) : 0;
     if (cur.k0 < nI) {
       ok = load_q() && load_limbs(0);
-      for (int k = cur.k0; ok && k < nI; ++k) ok = load_codes(k) && (k < cur.k0 + 2 || skip(2));  // packed pages run ahead
-      ok = ok && skip(2 * min(2, nI - cur.k0)) && (C.P.absorbed || load_limbs(1));
+      if constexpr (MODE == kDequant) {
+        for (int k = cur.k0; ok && k < nI; ++k) ok = load_codes(k) && (k < cur.k0 + 2 || skip(2));  // packed pages run ahead
+        ok = ok && skip(2 * min(2, nI - cur.k0));
+      } else if constexpr (MODE == kTiles) {
+        for (int k = cur.k0; ok && k < nI; ++k) ok = load_tiles(k);
+      }
+      ok = ok && (C.P.absorbed || load_limbs(1));
     }
     const int kb = max(cur.k0, nI);
     if (ok && kb < cur.k1) {
@@ -501,14 +528,14 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MIXED>*
       for (int k = kb; ok && k < cur.k1; ++k) ok = load_block(k);
     }
   }
-  if (!ok) {  // never leave with a copy in flight
-    for (int s = 0; s < kStages<MIXED>; ++s)
-      if ((issued >> s) & 1) mbar_wait(&sh->full[s], (last_parity >> s) & 1, C.err);
-    if (qn) mbar_wait(&sh->q_full, (qn - 1) & 1, C.err);
-    if constexpr (MIXED) {
-      const uint32_t slots = code_slots(C.P);
-      for (uint32_t c = cpos > slots ? cpos - slots : 0; c < cpos; ++c) mbar_wait(&sh->code_full[c % slots], (c / slots) & 1, C.err);
-    }
+  // Never leave with a copy in flight, whoever gave up: wait for the last lap's tiles, queries and
+  // packed pages.
+  for (int s = 0; s < kStages<MODE>; ++s)
+    if ((issued >> s) & 1) mbar_wait(&sh->full[s], (last_parity >> s) & 1, C.err);
+  if (qn) mbar_wait(&sh->q_full, (qn - 1) & 1, C.err);
+  if constexpr (MODE == kDequant) {
+    const uint32_t slots = code_slots(C.P);
+    for (uint32_t c = cpos > slots ? cpos - slots : 0; c < cpos; ++c) mbar_wait(&sh->code_full[c % slots], (c / slots) & 1, C.err);
   }
 }
 
@@ -517,8 +544,8 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MIXED>*
 __device__ __forceinline__ uint32_t nonfinite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 
 // ---- cleaning warps (two): a V tile at a time, 64 rows each, while the tile's scores become P ------
-template <bool MIXED>
-__device__ void clean_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* ring, int part, int lane) {
+template <int MODE>
+__device__ void clean_role(const ChunkArgs& C, Shared<MODE>* sh, uint8_t* ring, int part, int lane) {
   for (uint32_t n = 0;; ++n) {
     if (!wait_warp<true>(&sh->clean_go, n & 1, sh, C.err)) return;
     const Clean w = sh->clean;
@@ -571,17 +598,17 @@ __device__ void clean_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* ring,
 }
 
 // ---- tensor-core warp --------------------------------------------------------------------------
-template <bool MIXED>
-__device__ void mma_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq, uint8_t* ring, Cursor<MIXED> cur, int lane) {
+template <int MODE>
+__device__ void mma_role(const ChunkArgs& C, Shared<MODE>* sh, uint8_t* sq, uint8_t* ring, Cursor<MODE> cur, int lane) {
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem, 0), aq = smem_u32(sq), ar = smem_u32(ring);
   const uint32_t one = elect_one();
-  Ring<MIXED> r;
+  Ring<MODE> r;
   uint32_t qn = 0, pn[2] = {0, 0}, seg = 0, cn = 0;
   bool ok = true;
   auto S = [&](int u) { return tmem + (uint32_t)(u * kTile); };
   auto O = [&](int u) { return tmem + (uint32_t)(2 * kTile + u * kTile); };
   auto wait_full = [&](uint32_t pos) {
-    const bool w = wait_warp(&sh->full[pos % kStages<MIXED>], (pos / kStages<MIXED>) & 1, sh, C.err);
+    const bool w = wait_warp(&sh->full[pos % kStages<MODE>], (pos / kStages<MODE>) & 1, sh, C.err);
     tc_fence_after();
     return w;
   };
@@ -590,7 +617,7 @@ __device__ void mma_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq, uin
     tc_fence_after();
     return w;
   };
-  auto addr = [&](uint32_t pos) { return ar + (__shfl_sync(0xffffffffu, pos, 0) % kStages<MIXED>) * kTileBytes; };
+  auto addr = [&](uint32_t pos) { return ar + (__shfl_sync(0xffffffffu, pos, 0) % kStages<MODE>) * kTileBytes; };
   auto qk = [&](int u, uint32_t b, uint32_t idesc, bool acc) {
     tc_gemm_ss(S(u), desc_k(aq + u * kTileBytes), desc_k(b), idesc, acc, one);
   };
@@ -602,7 +629,7 @@ __device__ void mma_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq, uin
   for (; ok && cur.valid(); cur.next(C)) {
     if (cur.empty()) continue;
     const int tiles = cur.two() ? 2 : 1, sb = seg++ & 1;
-    const int nI = MIXED ? min(cur.k1, cur.s.nI) : 0;
+    const int nI = MODE != kBf16 ? min(cur.k1, cur.s.nI) : 0;
     if (lane < 16) sh->bad[sb][lane >> 2][lane & 3] = 0;
     if (lane == 0) sh->any_bad[sb] = 0;
     __syncwarp();
@@ -617,7 +644,7 @@ __device__ void mma_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq, uin
         qk(u, addr(kpos), idesc, false);
         commit(&sh->s_full[u]);
       }
-      commit(&sh->empty[kpos % kStages<MIXED>]);
+      commit(&sh->empty[kpos % kStages<MODE>]);
       if (a + 1 == b) commit(&sh->q_empty);
       for (int k = a; k < b; ++k) {
         const uint32_t vpos = kpos + 1;
@@ -626,8 +653,8 @@ __device__ void mma_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq, uin
         if (idesc == kIdescBf16) {
           Clean w;
           w.lo = w.hi = w.slot = 0;
-          if (MIXED && k < cur.s.nI + cur.s.nB) {
-            const Half h0 = half_of<MIXED>(cur.s, k, 0), h1 = half_of<MIXED>(cur.s, k, 1);
+          if (MODE != kBf16 && k < cur.s.nI + cur.s.nB) {
+            const Half h0 = half_of<MODE>(cur.s, k, 0), h1 = half_of<MODE>(cur.s, k, 1);
             w.a[0] = h0.lo, w.b[0] = h0.hi, w.a[1] = h1.lo, w.b[1] = h1.hi;
           } else {  // the diagonal: some rows of the pair see a key and others do not
             const int j = k - cur.s.nI - cur.s.nB;
@@ -638,7 +665,7 @@ __device__ void mma_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq, uin
           }
           dirty = w.lo < w.hi || w.a[0] > 0 || w.a[1] > 0 || w.b[0] < 64 || w.b[1] < 64;
           if (dirty && lane == 0) {
-            w.stage = vpos % kStages<MIXED>;
+            w.stage = vpos % kStages<MODE>;
             sh->clean = w;
             mbar_arrive(&sh->clean_go);
           }
@@ -654,15 +681,15 @@ __device__ void mma_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq, uin
           commit(k + 1 < b ? &sh->s_full[u] : &sh->o_full[u]);  // the next S, or behind the last block O
         }
         acc = true;
-        commit(&sh->empty[vpos % kStages<MIXED>]);
+        commit(&sh->empty[vpos % kStages<MODE>]);
         kpos = vpos + 1;
-        if (k + 1 < b) commit(&sh->empty[kpos % kStages<MIXED>]);
+        if (k + 1 < b) commit(&sh->empty[kpos % kStages<MODE>]);
         if (k + 2 == b) commit(&sh->q_empty);
       }
       r.pos = kpos;
       return true;
     };
-    if (MIXED && cur.k0 < nI) {
+    if (MODE != kBf16 && cur.k0 < nI) {
       ok = wait_warp(&sh->q_full, qn++ & 1, sh, C.err) && wait_full(r.pos) && wait_full(r.pos + 1);
       if (!ok) break;
       for (int u = 0; u < tiles; ++u) {
@@ -670,8 +697,8 @@ __device__ void mma_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq, uin
         qk(u, addr(r.pos + 1), kIdescBf16, true);
         commit(&sh->s_full[u]);
       }
-      commit(&sh->empty[r.pos % kStages<MIXED>]);
-      commit(&sh->empty[(r.pos + 1) % kStages<MIXED>]);
+      commit(&sh->empty[r.pos % kStages<MODE>]);
+      commit(&sh->empty[(r.pos + 1) % kStages<MODE>]);
       r.pos += kLimbs;
       for (int u = 0; ok && u < tiles; ++u) ok = wait_p(u);  // Q R_K is in shared memory
       ok = ok && blocks(cur.k0, nI, kIdescBase);
@@ -686,8 +713,8 @@ __device__ void mma_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq, uin
           pv(u, S(u) + 64, addr(r.pos), kIdescBf16, true);
           if (nI == cur.k1) commit(&sh->o_full[u]);
         }
-        commit(&sh->empty[r.pos % kStages<MIXED>]);
-        commit(&sh->empty[(r.pos + 1) % kStages<MIXED>]);
+        commit(&sh->empty[r.pos % kStages<MODE>]);
+        commit(&sh->empty[(r.pos + 1) % kStages<MODE>]);
         r.pos += kLimbs;
       }
     }
@@ -736,8 +763,8 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* w, bool wide) {
   }
 }
 
-template <bool MIXED>
-__device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq, const Cursor<MIXED>& start, int u) {
+template <int MODE>
+__device__ void softmax_role(const ChunkArgs& C, Shared<MODE>* sh, uint8_t* sq, const Cursor<MODE>& start, int u) {
   const int row = threadIdx.x & 127, warp = row >> 5;
   const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
   const uint32_t tS = sh->tmem + lane_off + u * kTile, tO = sh->tmem + lane_off + 2 * kTile + u * kTile;
@@ -745,7 +772,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
   bool ok = true;
   const int hg = C.hg, tpt = kTile / hg;
   // this warp's cursor, moved by its first lane
-  Cursor<MIXED>& cur = sh->cursors[threadIdx.x >> 5];
+  Cursor<MODE>& cur = sh->cursors[threadIdx.x >> 5];
   if ((threadIdx.x & 31) == 0) cur = start;
   __syncwarp();
   auto next = [&]() {
@@ -788,7 +815,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
       continue;
     }
     const int lim = min(cur.s.A + tok + 1, cur.s.A + cur.s.n);  // keys of the causal blocks this row sees
-    const int nI = MIXED ? min(cur.k1, cur.s.nI) : 0;
+    const int nI = MODE != kBf16 ? min(cur.k1, cur.s.nI) : 0;
     float m = -INFINITY, l = 0.f;
     bool have = false;  // O holds something
 
@@ -797,8 +824,8 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
       // scores of columns this row may not see
       uint64_t b0 = ~0ull, b1 = ~0ull;
       bool masked;
-      if (MIXED && k < cur.s.nI + cur.s.nB) {
-        const Half h0 = half_of<MIXED>(cur.s, k, 0), h1 = half_of<MIXED>(cur.s, k, 1);
+      if (MODE != kBf16 && k < cur.s.nI + cur.s.nB) {
+        const Half h0 = half_of<MODE>(cur.s, k, 0), h1 = half_of<MODE>(cur.s, k, 1);
         b0 = bits(h0.lo, h0.hi);
         b1 = bits(h1.lo, h1.hi);
         masked = (b0 & b1) != ~0ull;
@@ -876,7 +903,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
       };
       bool fresh = __any_sync(0xffffffffu, m == -INFINITY);
       const float2 sc2 = make_float2(scale, scale);
-      if constexpr (MIXED) {
+      if constexpr (MODE == kDequant) {
       bool again = fresh;
 #pragma unroll 1
       for (int c = 0;;) {
@@ -945,7 +972,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
       return true;
     };
 
-    if (MIXED && cur.k0 < nI) {
+    if (MODE != kBf16 && cur.k0 < nI) {
       // Q R_K: fp16, scaled by the power of two that brings the row's largest value to [1, 2)
       ok = wait_s();
       if (!ok) break;
@@ -1013,7 +1040,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
     for (int k = kb; ok && k < cur.k1; ++k) ok = block(std::false_type{}, k, kScoreLog2);
     if (!ok) break;
     // O is complete (behind the last INT2 block of an absorbed pool it was waited for above)
-    if (kb < cur.k1 || (MIXED && !C.P.absorbed)) ok = wait_o();
+    if (kb < cur.k1 || (MODE != kBf16 && !C.P.absorbed)) ok = wait_o();
     if (!ok) break;
 
     const bool bad = *reinterpret_cast<volatile uint32_t*>(&sh->any_bad[sb]) != 0;
@@ -1044,7 +1071,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
           if (key >= lim || !((sh->bad[sb][b >> 7][(b >> 5) & 3] >> (b & 31)) & 1)) continue;
           const __nv_bfloat16* v;
           int swz = 0;
-          if constexpr (MIXED) {
+          if constexpr (MODE != kBf16) {
             v = C.v_new + ((int64_t)(cur.s.row0 + key) * C.Hkv + cur.h) * kHeadDim;
           } else {
             int64_t pid = C.page_table[(int64_t)cur.i * C.max_pages + (key >> 6)];
@@ -1082,46 +1109,14 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MIXED>* sh, uint8_t* sq,
 }
 
 // ---- dequantising warps (pool) -------------------------------------------------------------------
-// What turns a group's codes into fp16 values: scale and zero, or with a Lloyd-Max codebook the four
-// values as two words that a byte selector picks from (fp32 products, one rounding).
-struct Levels {
-  uint32_t a, b;
-};
-__device__ __forceinline__ Levels levels(uint32_t sz, float l1, bool table) {
-  Levels r;
-  if (table) {
-    const float s = half_lo(sz), z = half_hi(sz);
-    r.a = pack_half2(z, fmaf(l1, s, z));
-    r.b = pack_half2(fmaf(3.f - l1, s, z), fmaf(3.f, s, z));
-  } else {
-    r.a = __byte_perm(sz, sz, 0x1010);
-    r.b = __byte_perm(sz, sz, 0x3232);
-  }
-  return r;
-}
-// Slot p (bits 2p, 2p + 1 of either 16-bit half) of x as an f16x2 pair of values. Uniform levels: the
-// code bits under the exponent of 2^(10 - 2p) are 2^(10 - 2p) + code, exactly; one subtraction and
-// one fused multiply-add (one rounding) make code * s + z.
-__device__ __forceinline__ uint32_t expand(uint32_t x, int p, const Levels& t, bool table) {
-  if (table) {
-    const uint32_t sel = ((x >> (2 * p)) & 0x00030003u) * 0x22u + 0x00100010u;  // nibbles 2c, 2c + 1 per code
-    return __byte_perm(t.a, t.b, __byte_perm(sel, 0, 0x4420));
-  }
-  const uint32_t base = (0x6400u - 0x800u * p) * 0x10001u;
-  const uint32_t h = (x & (0x00030003u << (2 * p))) | base;
-  const __half2 c = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&base));
-  const __half2 v = __hfma2(c, *reinterpret_cast<const __half2*>(&t.a), *reinterpret_cast<const __half2*>(&t.b));
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ void dequant_role(const ChunkArgs& C, Shared<true>* sh, uint8_t* ring, const uint8_t* codes, Cursor<true> cur) {
+__device__ void dequant_role(const ChunkArgs& C, Shared<kDequant>* sh, uint8_t* ring, const uint8_t* codes, Cursor<kDequant> cur) {
   const int x = threadIdx.x & 127, lane = threadIdx.x & 31;
   const DevPool& P = C.P;
   const int ng = P.ngroups, slots = code_slots(P);
   // K: thread x has token x of the block. V: a slice of 16 tokens, of it tokens 8u + 2tq + {0, 1} and
   // one half of the dims.
   const int slice = x >> 4, wh = (x >> 3) & 1, uu = (x >> 2) & 1, tq = x & 3;
-  Ring<true> r;
+  Ring<kDequant> r;
   uint32_t cpos = 0;
   bool ok = true;
   auto done = [&](uint64_t* bar) {
@@ -1231,8 +1226,8 @@ __device__ void dequant_role(const ChunkArgs& C, Shared<true>* sh, uint8_t* ring
 }
 
 // ------------------------------------------------------------------------------------------------
-template <bool MIXED>
-constexpr int kChunkThreads = MIXED ? 512 : 384;
+template <int MODE>
+constexpr int kChunkThreads = MODE == kDequant ? 512 : 384;
 
 template <int R>
 __device__ __forceinline__ void reg_inc() {
@@ -1251,16 +1246,16 @@ __device__ __forceinline__ int64_t boundary(int c, int64_t total, int n) {
 
 // Units of all sequences, this CTA's range [g0, g1) of them and the item that holds g0; every thread
 // of the CTA. Returns the number of CTAs that have a range.
-template <bool MIXED>
-__device__ int plan(const ChunkArgs& C, Shared<MIXED>* sh, int64_t& g0, int64_t& g1) {
-  constexpr int NT = kChunkThreads<MIXED>, NW = NT / 32;
+template <int MODE>
+__device__ int plan(const ChunkArgs& C, Shared<MODE>* sh, int64_t& g0, int64_t& g1) {
+  constexpr int NT = kChunkThreads<MODE>, NW = NT / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the first NT sequences stay in registers for the second pass
   SeqWork s0{};
-  if (threadIdx.x < C.n_seqs) s0 = load_seq<MIXED>(C, threadIdx.x);
+  if (threadIdx.x < C.n_seqs) s0 = load_seq<MODE>(C, threadIdx.x);
   const int64_t per0 = units_of(s0, C.lg);
   int64_t mine = per0 * C.Hkv, total = 0;
-  for (int i = threadIdx.x + NT; i < C.n_seqs; i += NT) mine += units_of(load_seq<MIXED>(C, i), C.lg) * C.Hkv;
+  for (int i = threadIdx.x + NT; i < C.n_seqs; i += NT) mine += units_of(load_seq<MODE>(C, i), C.lg) * C.Hkv;
 #pragma unroll
   for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) sh->scan[warp] = mine;
@@ -1279,7 +1274,7 @@ __device__ int plan(const ChunkArgs& C, Shared<MIXED>* sh, int64_t& g0, int64_t&
     int64_t per = per0;
     if (i0) {
       s = SeqWork{};
-      if (i < C.n_seqs) s = load_seq<MIXED>(C, i);
+      if (i < C.n_seqs) s = load_seq<MODE>(C, i);
       per = units_of(s, C.lg);
     }
     const int64_t cnt = per * C.Hkv;
@@ -1320,17 +1315,17 @@ __device__ int plan(const ChunkArgs& C, Shared<MIXED>* sh, int64_t& g0, int64_t&
   return n;
 }
 
-template <bool MIXED>
-__global__ void __launch_bounds__(kChunkThreads<MIXED>, 1)
+template <int MODE>
+__global__ void __launch_bounds__(kChunkThreads<MODE>, 1)
     k_chunk(const __grid_constant__ ChunkArgs C, const __grid_constant__ ChunkMaps M) {
   extern __shared__ __align__(1024) uint8_t smem[];  // tiles start on the swizzle's 1024-byte boundaries
-  uint8_t *sq = smem, *ring = smem + 2 * kTileBytes, *codes = ring + kStages<MIXED> * kTileBytes;
-  Shared<MIXED>* sh = reinterpret_cast<Shared<MIXED>*>(codes + (MIXED ? kCodeBuf : 0));
+  uint8_t *sq = smem, *ring = smem + 2 * kTileBytes, *codes = ring + kStages<MODE> * kTileBytes;
+  Shared<MODE>* sh = reinterpret_cast<Shared<MODE>*>(codes + (MODE == kDequant ? kCodeBuf : 0));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages<MIXED>; ++s) {
-      mbar_init(&sh->full[s], MIXED ? 4 : 1);
-      mbar_init(&sh->empty[s], MIXED ? 1 + kPassers : 1);
+    for (int s = 0; s < kStages<MODE>; ++s) {
+      mbar_init(&sh->full[s], MODE == kDequant ? 4 : 1);
+      mbar_init(&sh->empty[s], MODE == kDequant ? 1 + kPassers : 1);
     }
     for (int s = 0; s < kMaxSlots; ++s) {
       mbar_init(&sh->code_full[s], 1);
@@ -1350,7 +1345,7 @@ __global__ void __launch_bounds__(kChunkThreads<MIXED>, 1)
     fence_mbar_init();
   }
   int64_t g0, g1;
-  const int n = plan<MIXED>(C, sh, g0, g1);
+  const int n = plan<MODE>(C, sh, g0, g1);
   if (threadIdx.x == 0 && g0 >= g1) reinterpret_cast<Part*>(C.ws)[blockIdx.x].parts = 0;
   if (g0 >= g1) return;
   if (warp == 0) {
@@ -1360,7 +1355,7 @@ __global__ void __launch_bounds__(kChunkThreads<MIXED>, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  Cursor<MIXED> cur;
+  Cursor<MODE> cur;
   const int64_t x0 = sh->st_x;
   cur.start(C, sh->st_i, sh->st_h, sh->st_t, x0, g1 - g0);
   if (threadIdx.x == 0) {
@@ -1382,37 +1377,37 @@ __global__ void __launch_bounds__(kChunkThreads<MIXED>, 1)
     }
     reinterpret_cast<Part*>(C.ws)[blockIdx.x] = d;
   }
-  if constexpr (MIXED) {
+  if constexpr (MODE == kDequant) {
     // registers of the launch: 512 x 128 = 128 x (2 x 168 + 96 + 80)
     if (warp < 8) {
       reg_inc<168>();
-      softmax_role<true>(C, sh, sq, cur, warp >> 2);
+      softmax_role<MODE>(C, sh, sq, cur, warp >> 2);
     } else if (warp < 12) {
       reg_dec<96>();
       dequant_role(C, sh, ring, codes, cur);
     } else {
       reg_dec<80>();
       if (warp == 12) {
-        if (lane == 0) load_role<true>(C, M, sh, sq, ring, codes, cur);
+        if (lane == 0) load_role<MODE>(C, M, sh, sq, ring, codes, cur);
       } else if (warp == 13) {
-        mma_role<true>(C, sh, sq, ring, cur, lane);
+        mma_role<MODE>(C, sh, sq, ring, cur, lane);
       } else {
-        clean_role<true>(C, sh, ring, warp - 14, lane);
+        clean_role<MODE>(C, sh, ring, warp - 14, lane);
       }
     }
   } else {
     // 384 x 168 = 128 x (2 x 208 + 88)
     if (warp < 8) {
       reg_inc<208>();
-      softmax_role<false>(C, sh, sq, cur, warp >> 2);
+      softmax_role<MODE>(C, sh, sq, cur, warp >> 2);
     } else {
       reg_dec<88>();
       if (warp == 8) {
-        if (lane == 0) load_role<false>(C, M, sh, sq, ring, codes, cur);
+        if (lane == 0) load_role<MODE>(C, M, sh, sq, ring, codes, cur);
       } else if (warp == 9) {
-        mma_role<false>(C, sh, sq, ring, cur, lane);
+        mma_role<MODE>(C, sh, sq, ring, cur, lane);
       } else {
-        clean_role<false>(C, sh, ring, warp - 10, lane);
+        clean_role<MODE>(C, sh, ring, warp - 10, lane);
       }
     }
   }
@@ -1495,7 +1490,7 @@ void set_buffers(ChunkArgs& C, void* workspace, void* out) {
 
 // One CTA per SM of the current device (0: a CUDA call failed); the kernel's shared memory is asked
 // for on the first call per device.
-template <bool MIXED>
+template <int MODE>
 int chunk_ctas() {
   constexpr int kDevices = 64;
   static std::atomic<int> ctas[kDevices];  // 0: not set up
@@ -1503,18 +1498,18 @@ int chunk_ctas() {
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (dev < kDevices && (sms = ctas[dev].load(std::memory_order_relaxed)) > 0) return sms;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      cudaFuncSetAttribute(k_chunk<MIXED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem<MIXED>) != cudaSuccess)
+      cudaFuncSetAttribute(k_chunk<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem<MODE>) != cudaSuccess)
     return 0;
   sms = sms < kMaxCtas ? sms : kMaxCtas;
   if (dev < kDevices) ctas[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 
-template <bool MIXED>
+template <int MODE>
 cudaError_t launch_chunk(const ChunkArgs& C, const ChunkMaps& M, cudaStream_t s) {
-  const int ctas = chunk_ctas<MIXED>();
+  const int ctas = chunk_ctas<MODE>();
   if (ctas < 1) return cudaErrorUnknown;
-  k_chunk<MIXED><<<ctas, kChunkThreads<MIXED>, kChunkSmem<MIXED>, s>>>(C, M);
+  k_chunk<MODE><<<ctas, kChunkThreads<MODE>, kChunkSmem<MODE>, s>>>(C, M);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
   k_chunk_join<<<dim3(ctas, C.rows / kJoinRows), 256, 0, s>>>(C);
@@ -1528,8 +1523,8 @@ size_t chunk_workspace_bytes(int hg, int64_t n_tokens) {
   return 32 + (size_t)kMaxCtas * (kDescBytes + 2 * (size_t)slot_rows(hg, n_tokens) * (kHeadDim + 2) * 4);
 }
 
-cudaError_t launch_chunk_pool(const DevPool& P, const StepDims& S, int layer, bool skip_single, const void* q,
-                              const void* k_new, const void* v_new, void* workspace, void* out, cudaStream_t s) {
+cudaError_t launch_chunk_pool(const DevPool& P, const StepDims& S, int layer, bool skip_single, const ChunkTiles* tiles,
+                              const void* q, const void* k_new, const void* v_new, void* workspace, void* out, cudaStream_t s) {
   ChunkArgs C{};
   C.Hq = P.Hq;
   C.Hkv = P.Hkv;
@@ -1554,7 +1549,10 @@ cudaError_t launch_chunk_pool(const DevPool& P, const StepDims& S, int layer, bo
       !map_pages(&M.ring_k, P.ring_k + (size_t)layer * P.ring_layer_stride, ring_rows) ||
       !map_pages(&M.ring_v, P.ring_v + (size_t)layer * P.ring_layer_stride, ring_rows))
     return cudaErrorUnknown;
-  return launch_chunk<true>(C, M, s);
+  if (!tiles) return launch_chunk<kDequant>(C, M, s);
+  C.tiles = tiles->tiles;
+  C.tile_base = tiles->base;
+  return launch_chunk<kTiles>(C, M, s);
 }
 
 }  // namespace oscar
@@ -1611,7 +1609,7 @@ oscar_status oscar_bf16_chunk(int32_t num_q_heads, int32_t num_kv_heads, int32_t
   if (!map_rows(&M.q, q, num_q_heads, n_tokens, q_token_stride, C.hg, kTile / C.hg) || !map_pages(&M.k, k_pages, rows) ||
       !map_pages(&M.v, v_pages, rows))
     return OSCAR_ECUDA;
-  const cudaError_t e = launch_chunk<false>(C, M, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_chunk<kBf16>(C, M, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return OSCAR_ECUDA;

@@ -129,8 +129,18 @@ cudaError_t launch_merge_new(const DevPool& P, const StepDims& S, int layer, con
 // Attention of new tokens over a cache (chunk.cu). workspace: chunk_workspace_bytes() bytes.
 // skip_single: leave out the sequences of one new token.
 size_t chunk_workspace_bytes(int hg, int64_t n_tokens);
-cudaError_t launch_chunk_pool(const DevPool& P, const StepDims& S, int layer, bool skip_single, const void* q,
-                              const void* k_new, const void* v_new, void* workspace, void* out, cudaStream_t s);
+struct ChunkTiles {          // the histories as fp16 tiles (chunk_tiles.cu)
+  const uint8_t* tiles;      // [blocks of 128 tokens of every sequence: KV head, block][K, V]
+  const int32_t* base;       // first block of sequence i (n_seqs + 1)
+};
+// tiles: null, and the chunk kernel dequantises the packed pages itself.
+cudaError_t launch_chunk_pool(const DevPool& P, const StepDims& S, int layer, bool skip_single, const ChunkTiles* tiles,
+                              const void* q, const void* k_new, const void* v_new, void* workspace, void* out,
+                              cudaStream_t s);
+size_t chunk_tiles_workspace_bytes(const DevPool& P, const StepDims& S, int64_t blocks);
+// Make the tiles of the step's sequences (blocks of them, as the host counted) in workspace.
+cudaError_t launch_chunk_tiles(const DevPool& P, const StepDims& S, int layer, bool skip_single, int64_t blocks,
+                               void* workspace, ChunkTiles* out, cudaStream_t s);
 // The sequences of one new token by the decode kernels (chunk_single.cu). S1: their batch before the
 // step (n_seqs, n_pairs, total_units, nw_max and nw of it).
 size_t chunk_single_workspace_bytes(const DevPool& P, const StepDims& S1);

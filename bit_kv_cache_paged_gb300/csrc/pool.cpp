@@ -158,6 +158,14 @@ namespace {
 // and 32.5 us.
 constexpr int64_t kSingleMinPagesPerSm = 4;
 
+// Histories are made into fp16 tiles before the chunk kernel when each block is used by this many pairs
+// of query tiles on average, and the tiles (64 KB a block and KV head) take no more than 4 GB. Measured,
+// tiles against dequantising in the kernel, one sequence after 16000 tokens, 4 query heads a KV head: 4
+// pairs 99.7 and 91.0 us, 6 pairs 117.6 and 116.2, 8 pairs 141 and 146, 16 pairs 232 and 267; eight
+// sequences after 4000: 2 pairs 117 and 109, 4 pairs 192 and 212.
+constexpr int64_t kTilesMinUses = 5;
+constexpr size_t kTilesMaxBytes = (size_t)4 << 30;
+
 oscar_status cuda_fail(cudaError_t e) {
   if (e == cudaSuccess) return OSCAR_OK;
   (void)cudaGetLastError();
@@ -636,7 +644,8 @@ oscar_status oscar_rotate_q(oscar_pool* p, int32_t layer, const void* q, float* 
 struct ChunkPlan {
   StepDims single;  // the single-token sequences' batch, before the step (n_seqs 0: none apart)
   bool chunk;       // rows for the chunk kernel
-  size_t chunk_bytes, single_bytes;
+  int64_t tiles;    // blocks of 128 history tokens made into fp16 tiles for it (0: it dequantises itself)
+  size_t chunk_bytes, single_bytes, tiles_bytes;
 };
 
 static ChunkPlan chunk_plan(const oscar_pool* p) {
@@ -657,6 +666,21 @@ static ChunkPlan chunk_plan(const oscar_pool* p) {
     c.single_bytes = chunk_single_workspace_bytes(p->P, d);
   }
   c.chunk = p->dims.total_new > c.single.n_seqs;
+  if (c.chunk) {
+    const int pair = 256 / p->hg;  // tokens of a pair of query tiles
+    int64_t blocks = 0, uses = 0;
+    for (const StepSeq& s : p->step) {
+      const int64_t n = s.L_new - s.L_old, b = (s.F_old - kSink + 127) / 128;
+      if (n == 0 || (n == 1 && c.single.n_seqs > 0)) continue;
+      blocks += b;
+      uses += b * ((n + pair - 1) / pair);
+    }
+    const size_t bytes = align_up(chunk_tiles_workspace_bytes(p->P, p->dims, blocks));
+    if (blocks > 0 && uses >= kTilesMinUses * blocks && bytes <= kTilesMaxBytes) {
+      c.tiles = blocks;
+      c.tiles_bytes = bytes;
+    }
+  }
   c.chunk_bytes = c.chunk ? align_up(chunk_workspace_bytes(p->hg, p->dims.total_new)) : 0;
   return c;
 }
@@ -664,7 +688,7 @@ static ChunkPlan chunk_plan(const oscar_pool* p) {
 size_t oscar_chunk_workspace_bytes(const oscar_pool* p) {
   if (!p || !p->in_step || p->host_only) return 0;
   const ChunkPlan c = chunk_plan(p);
-  return c.chunk_bytes + c.single_bytes + kAlign;
+  return c.chunk_bytes + c.single_bytes + c.tiles_bytes + kAlign;
 }
 
 oscar_status oscar_chunk_attend(oscar_pool* p, int32_t layer, const void* q, const void* k_new, const void* v_new,
@@ -689,7 +713,14 @@ oscar_status oscar_chunk_attend(oscar_pool* p, int32_t layer, const void* q, con
     p->launch_count += n;
   }
   if (e == cudaSuccess && c.chunk) {
-    e = launch_chunk_pool(p->P, p->dims, layer, c.single.n_seqs > 0, q, k_new, v_new, ws, out, st);
+    const bool apart = c.single.n_seqs > 0;
+    ChunkTiles tiles;
+    if (c.tiles) {
+      e = launch_chunk_tiles(p->P, p->dims, layer, apart, c.tiles, ws + c.chunk_bytes + c.single_bytes, &tiles, st);
+      p->launch_count += 2;
+    }
+    if (e == cudaSuccess)
+      e = launch_chunk_pool(p->P, p->dims, layer, apart, c.tiles ? &tiles : nullptr, q, k_new, v_new, ws, out, st);
     p->launch_count += 2;
   }
   return cuda_fail(e);

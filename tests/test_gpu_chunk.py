@@ -364,6 +364,28 @@ def test_pool_single_tokens_over_long_histories(group, absorbed, lloyd, hq):
     m.chunk([2, 0, 3, 6], [0, 1, 1, 130])
 
 
+@pytest.mark.parametrize("group,absorbed,lloyd,hq", [(128, False, None, 4), (32, False, None, 8), (128, True, None, 8), (32, True, (1.2, 0.8), 4),
+                                                     (128, False, (0.9, 1.3), 8)])
+def test_pool_long_chunks_over_histories(group, absorbed, lloyd, hq):
+    """Chunks long enough for their histories to be expanded beforehand, several sequences and one without a history."""
+    m = Mixed(hq=hq, hkv=1, group=group, absorbed=absorbed, lloyd=lloyd, seed=group + hq, max_seqs=5, max_len=6000)
+    ctx = [1500, 0, 385, 2049, 320]
+    for i in range(5):
+        m.add(i)
+    m.pool.step_begin(range(5), ctx)
+    kv = m.new_rows(sum(ctx))
+    m.pool.append_and_demote(0, kv[0][0], kv[1][0])
+    r = 0
+    for i, n in enumerate(ctx):
+        m.rows[i] = [x[:, r:r + n] for x in kv]
+        r += n
+    m.pool.step_begin(range(5), [0] * 5)
+    launches = m.pool.launch_count()
+    m.chunk([4, 3, 1, 0, 2], [600, 701, 900, 1025, 0])
+    assert m.pool.launch_count() - launches > 8  # two calls of four launches, and the append
+    m.chunk([0, 2, 3], [555, 513, 1])
+
+
 def test_pool_single_tokens_bad_value_and_bad_page():
     m = Mixed(hq=32, hkv=8, seed=22, max_seqs=4, max_len=4096)
     for i in range(4):
