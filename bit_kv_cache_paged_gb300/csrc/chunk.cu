@@ -62,7 +62,7 @@ constexpr int kDescBytes = 32;
 // a block of BF16 keys takes 3, one of INT2 keys 4; an item takes another 6 a tile (queries in, first
 // and masked blocks, output out), and 8 more a tile for its two rotations.
 constexpr int kUnitsBf16 = 3, kUnitsInt2 = 4, kUnitsTile = 6, kUnitsRotate = 8;
-constexpr int kMinUnits = 12;                 // per CTA, at least, before a call is cut further
+constexpr int kMinUnits = 4;  // per CTA, at least: a block and a little (64 tokens after 500: 28 us at 12, 20 at 3 to 6)
 
 constexpr uint32_t kIdescBase = (1u << 4) | ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
 constexpr uint32_t kIdescBf16 = kIdescBase | (1u << 7) | (1u << 10);  // A, B bf16; fp16 without these bits
@@ -1417,38 +1417,74 @@ __global__ void __launch_bounds__(kChunkThreads<MODE>, 1)
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sh->tmem));
 }
 
-// Join the parts of the items that CTA boundaries cut: block (c, y) takes 32 rows of the item that
+// Join the parts of the items that CTA boundaries cut: block (c, y) takes kJoinRows rows of the item that
 // boundary c cuts first. Part 0 is slot 1 of CTA c - 1, part p slot 0 of CTA c - 1 + p.
-constexpr int kJoinRows = 32;
+//
+// What bounds it is the wait for its loads: a warp takes two rows, two parts of each in flight. Few registers
+// (many blocks at once) count for more than deep loads: four rows and four parts at a time take 9 us more on
+// the ragged batch of 12 (142 us), one row and eight parts 6 us; with one part after another, the way from
+// 64 tokens after 500 is 7 us longer (21 us).
+constexpr int kJoinEach = 2, kJoinDepth = 2, kJoinRows = 8 * kJoinEach;
 __global__ void __launch_bounds__(256) k_chunk_join(const __grid_constant__ ChunkArgs C) {
   const Part d = reinterpret_cast<const Part*>(C.ws)[blockIdx.x];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (d.parts == 0) return;
+  const int row0 = blockIdx.y * kJoinRows + warp;
+  if (d.parts == 0 || row0 >= d.rows) return;
   const float* slots = reinterpret_cast<const float*>(C.ws + (size_t)kMaxCtas * kDescBytes);
   const size_t slot = (size_t)C.rows * (kHeadDim + 2);
   auto part = [&](int p) { return slots + ((size_t)(blockIdx.x - 1 + p) * 2 + (p == 0 ? 1 : 0)) * slot; };
-  for (int row = blockIdx.y * kJoinRows + warp; row < min(d.rows, (int)(blockIdx.y + 1) * kJoinRows); row += 8) {
-    float M = -INFINITY;
-    for (int p = lane; p < d.parts; p += 32) M = fmaxf(M, part(p)[(size_t)C.rows * kHeadDim + 2 * row]);
+  float M[kJoinEach], l[kJoinEach];
+  float4 acc[kJoinEach];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < d.parts; ++p) {
-      const float* s = part(p);
-      const float2 ml = *reinterpret_cast<const float2*>(s + (size_t)C.rows * kHeadDim + 2 * row);
-      const float4 o = *reinterpret_cast<const float4*>(s + (size_t)row * kHeadDim + 4 * lane);
-      if (ml.x == -INFINITY && ml.y == 0.f) continue;  // saw no key
-      const float w = fast_exp2(ml.x - M);
-      l += w * ml.y;
-      acc.x += w * o.x;
-      acc.y += w * o.y;
-      acc.z += w * o.z;
-      acc.w += w * o.w;
+  for (int r = 0; r < kJoinEach; ++r) {
+    M[r] = -INFINITY;
+    l[r] = 0.f;
+    acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int p0 = 0; p0 < d.parts; p0 += kJoinDepth) {
+    float2 ml[kJoinEach][kJoinDepth];
+    float4 o[kJoinEach][kJoinDepth];
+#pragma unroll
+    for (int i = 0; i < kJoinDepth; ++i) {
+#pragma unroll
+      for (int r = 0; r < kJoinEach; ++r) {
+        const int row = row0 + 8 * r;
+        ml[r][i] = make_float2(-INFINITY, 0.f);  // as of a part that saw no key
+        o[r][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p0 + i < d.parts && row < d.rows) {
+          const float* s = part(p0 + i);
+          ml[r][i] = *reinterpret_cast<const float2*>(s + (size_t)C.rows * kHeadDim + 2 * row);
+          o[r][i] = *reinterpret_cast<const float4*>(s + (size_t)row * kHeadDim + 4 * lane);
+        }
+      }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+#pragma unroll
+    for (int r = 0; r < kJoinEach; ++r) {
+      float top = M[r];
+#pragma unroll
+      for (int i = 0; i < kJoinDepth; ++i) top = fmaxf(top, ml[r][i].x);
+      const float old = M[r] == -INFINITY ? 0.f : fast_exp2(M[r] - top);
+      M[r] = top;
+      l[r] *= old;
+      acc[r] = make_float4(acc[r].x * old, acc[r].y * old, acc[r].z * old, acc[r].w * old);
+#pragma unroll
+      for (int i = 0; i < kJoinDepth; ++i) {
+        if (ml[r][i].x == -INFINITY && ml[r][i].y == 0.f) continue;
+        const float w = fast_exp2(ml[r][i].x - M[r]);
+        l[r] += w * ml[r][i].y;
+        acc[r].x += w * o[r][i].x;
+        acc[r].y += w * o[r][i].y;
+        acc[r].z += w * o[r][i].z;
+        acc[r].w += w * o[r][i].w;
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kJoinEach; ++r) {
+    const int row = row0 + 8 * r;
+    if (row >= d.rows) break;
+    const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[r].x * inv, acc[r].y * inv), b = __floats2bfloat162_rn(acc[r].z * inv, acc[r].w * inv);
     __nv_bfloat16* dst = C.out + ((int64_t)(d.row0 + row / C.hg) * C.Hq + d.head + row % C.hg) * kHeadDim + 4 * lane;
     *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   }
