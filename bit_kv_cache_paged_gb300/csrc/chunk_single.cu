@@ -8,8 +8,12 @@
 // and BF16 decodes and the merge run on it, the merge with the new token itself as one more key.
 // Memory bounds it (72 or 96 bytes per history token and KV head).
 //
-// Measured at 8 sequences of 32K history, 32 query and 8 KV heads, group 128: 224 us in chunk.cu, 61 us
-// here (the packed pages alone take 24 us at the copy peak, and the decode kernels read them at 70% of it).
+// The BF16 decode needs nothing from the rotation: outside a capture it runs beside it on a branch, joined
+// before the merge (64 us a call, 72 without).
+//
+// Measured at 8 sequences of 32K history, 32 query and 8 KV heads, group 128: 224 us in chunk.cu, here 64 us a
+// call, 60 replayed: view 3, rotation 6, BF16 decode 8, INT2 decode 41 (the packed pages alone take 24 us at the
+// copy peak; the decode kernel is bound by the unpacking of its codes), merge 11, each with a cold cache.
 #include "device_common.cuh"
 
 namespace oscar {
@@ -104,7 +108,7 @@ size_t chunk_single_workspace_bytes(const DevPool& P, const StepDims& S1) { retu
 
 cudaError_t launch_chunk_single(const DevPool& P, const StepDims& S, const StepDims& S1, int layer,
                                 const void* q, const void* k_new, const void* v_new, void* workspace, void* out,
-                                cudaStream_t s, int* launches) {
+                                const ChunkBranch& branch, cudaStream_t s, int* launches) {
   const SingleBuffers b = single_buffers(P, S1);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   StepDims* dims = reinterpret_cast<StepDims*>(ws + b.dims);
@@ -125,9 +129,24 @@ cudaError_t launch_chunk_single(const DevPool& P, const StepDims& S, const StepD
     e = r;
     ++*launches;
   };
+  const bool beside = e == cudaSuccess && branch.side;
+  cudaStream_t bs = beside ? branch.side : s;
+  if (beside) {
+    e = cudaEventRecord(branch.fork, s);
+    if (e == cudaSuccess) e = cudaStreamWaitEvent(bs, branch.fork, 0);
+    if (e != cudaSuccess) return e;
+  }
+  if (e == cudaSuccess) then(launch_decode_bf16(V, S1, layer, q1, pbf16, bs));
+  if (beside) {
+    const cudaError_t r = cudaEventRecord(branch.join, bs);
+    if (e == cudaSuccess) e = r;
+  }
   if (e == cudaSuccess) then(launch_rotate_q(V, S1, layer, q1, q_rot, s));
-  if (e == cudaSuccess) then(launch_decode_bf16(V, S1, layer, q1, pbf16, s));
   if (e == cudaSuccess) then(launch_decode_int2(V, S1, layer, q_rot, pint2, s));
+  if (beside) {
+    const cudaError_t r = cudaStreamWaitEvent(s, branch.join, 0);  // the branch joins even after an error
+    if (e == cudaSuccess) e = r;
+  }
   if (e == cudaSuccess) then(launch_merge_new(V, S1, layer, pint2, pbf16, q1, k_new, v_new, out, s));
   return e;
 }

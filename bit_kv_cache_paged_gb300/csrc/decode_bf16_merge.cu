@@ -375,7 +375,8 @@ __device__ __forceinline__ void load_bf16x4(const __nv_bfloat16* p, float (&x)[4
 // (kRowWarps / WPR rows per CTA). The warps of a row each softmax-combine every WPR-th INT2 split
 // (rotated basis) and the first one joins their results through shared memory; then the
 // un-rotation by U_V^T staged in shared memory, and the merge with the BF16 partial. Two warps
-// per row serve steps with many splits per row (few sequences), one warp the others. NEW: the row's own
+// per row serve steps with many splits per row (few sequences), one warp the others; with NEW four in the
+// place of two (8 sequences of 32K, 38 splits a row: 60.5 us the whole call, 61.8 with two). NEW: the row's own
 // new token joins as one more key (its score from q, k_new and v_new rows at the sequence's in_offset),
 // and the output goes to that row in bf16.
 template <int HG, int WPR, bool NEW>
@@ -456,7 +457,7 @@ __global__ void __launch_bounds__(kRowWarps * 32)
   }
   if (!P.absorbed) {
     // o . R_V^T = ((o P) H) U^T : permute, Walsh-Hadamard, then the basis back-rotation
-    float t[1][4], y[1][4];
+    float t[1][4], y[1][4] = {};
 #pragma unroll
     for (int e = 0; e < 4; ++e) buf[4 * lane + e] = oi[0][e];
     __syncwarp();
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     fwht128(t[0], lane);
     __syncthreads();
     if (!__all_sync(0xffffffffu, mbar_wait(bar, 0, P.err))) return;
-    matvec_u<1>(t, sU, y, lane);
+    if (part == 0) matvec_u<1>(t, sU, y, lane);  // 64 KB of shared memory a warp
 #pragma unroll
     for (int e = 0; e < 4; ++e) oi[0][e] = y[0][e];
   }
@@ -560,18 +561,19 @@ template <bool NEW>
 cudaError_t launch_merge_t(const DevPool& P, const StepDims& S, int layer, const float* partials_int2,
                            const float* partials_bf16, float* out, const NewRows& N, cudaStream_t s) {
   if (S.n_pairs <= 0) return cudaSuccess;
-  const int wpr = merge_wpr(S), rpc = kRowWarps / wpr;
+  const int wpr = NEW && merge_wpr(S) > 1 ? 4 : merge_wpr(S), rpc = kRowWarps / wpr;
   dim3 grid((S.n_seqs * P.hg + rpc - 1) / rpc, P.Hkv);
   const int smem = kUBytes + 16 + kRowWarps * kHeadDim * 4 + (wpr > 1 ? kRowWarps * (2 + kHeadDim) * 4 : 0);
   auto go = [&](auto kernel) {
     cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     kernel<<<grid, kRowWarps * 32, smem, s>>>(P, S, layer, partials_int2, partials_bf16, out, N);
   };
+  constexpr int kSome = NEW ? 4 : 2;
   if (P.hg == 4) {
-    if (wpr > 1) go(k_merge<4, 2, NEW>);
+    if (wpr > 1) go(k_merge<4, kSome, NEW>);
     else go(k_merge<4, 1, NEW>);
   } else {
-    if (wpr > 1) go(k_merge<8, 2, NEW>);
+    if (wpr > 1) go(k_merge<8, kSome, NEW>);
     else go(k_merge<8, 1, NEW>);
   }
   return cudaGetLastError();

@@ -142,11 +142,16 @@ size_t chunk_tiles_workspace_bytes(const DevPool& P, const StepDims& S, int64_t 
 cudaError_t launch_chunk_tiles(const DevPool& P, const StepDims& S, int layer, bool skip_single, int64_t blocks,
                                void* workspace, ChunkTiles* out, cudaStream_t s);
 // The sequences of one new token by the decode kernels (chunk_single.cu). S1: their batch before the
-// step (n_seqs, n_pairs, total_units, nw_max and nw of it).
+// step (n_seqs, n_pairs, total_units, nw_max and nw of it). side: where the BF16 decode may run beside
+// the query rotation (null: on s too), between the two events.
+struct ChunkBranch {
+  cudaStream_t side = nullptr;
+  cudaEvent_t fork = nullptr, join = nullptr;
+};
 size_t chunk_single_workspace_bytes(const DevPool& P, const StepDims& S1);
 cudaError_t launch_chunk_single(const DevPool& P, const StepDims& S, const StepDims& S1, int layer,
                                 const void* q, const void* k_new, const void* v_new, void* workspace, void* out,
-                                cudaStream_t s, int* launches);
+                                const ChunkBranch& branch, cudaStream_t s, int* launches);
 // INT2 decode workers (see step_begin)
 constexpr int kMaxPartialsPerPair = 64;  // per (sequence, KV head), on average, at most: bounds the merge's work
 __host__ __device__ inline int int2_workers(int64_t units, int64_t n_pairs, int64_t max_workers) {

@@ -143,6 +143,7 @@ struct oscar_pool {
   // a stream of its own for direct calls (a captured step uses capture_side), and its events
   cudaStream_t dec_side = nullptr;
   cudaEvent_t dec_fork = nullptr, dec_join = nullptr;
+  ChunkBranch chunk_branch;                 // the same for the single tokens of oscar_chunk_attend
   cudaGraphExec_t graph_exec = nullptr;
   GraphKey graph_key{};
   bool capturing = false;
@@ -458,6 +459,9 @@ oscar_status oscar_pool_destroy(oscar_pool* p) {
     if (p->dec_side) cudaStreamDestroy(p->dec_side);
     if (p->dec_fork) cudaEventDestroy(p->dec_fork);
     if (p->dec_join) cudaEventDestroy(p->dec_join);
+    if (p->chunk_branch.side) cudaStreamDestroy(p->chunk_branch.side);
+    if (p->chunk_branch.fork) cudaEventDestroy(p->chunk_branch.fork);
+    if (p->chunk_branch.join) cudaEventDestroy(p->chunk_branch.join);
     if (p->owns_arena && p->arena) cudaFree(p->arena);
   }
   delete p;
@@ -691,6 +695,20 @@ size_t oscar_chunk_workspace_bytes(const oscar_pool* p) {
   return c.chunk_bytes + c.single_bytes + c.tiles_bytes + kAlign;
 }
 
+// The branch for a call on st. None under capture: a stream that has joined a capture belongs to it until it
+// ends, and calls on other streams come here meanwhile.
+static cudaError_t chunk_branch(oscar_pool* p, cudaStream_t st, ChunkBranch* out) {
+  cudaStreamCaptureStatus capture;
+  cudaError_t e = cudaStreamIsCapturing(st, &capture);
+  if (e != cudaSuccess || capture != cudaStreamCaptureStatusNone) return e;
+  ChunkBranch& b = p->chunk_branch;
+  if (!b.fork) e = cudaEventCreateWithFlags(&b.fork, cudaEventDisableTiming);
+  if (e == cudaSuccess && !b.join) e = cudaEventCreateWithFlags(&b.join, cudaEventDisableTiming);
+  if (e == cudaSuccess && !b.side) e = cudaStreamCreateWithFlags(&b.side, cudaStreamNonBlocking);
+  if (e == cudaSuccess) *out = b;
+  return e;
+}
+
 oscar_status oscar_chunk_attend(oscar_pool* p, int32_t layer, const void* q, const void* k_new, const void* v_new,
                                 void* workspace, void* out, void* stream) {
   if (!p || layer < 0 || layer >= p->cfg.num_layers) return OSCAR_EINVAL;
@@ -709,7 +727,10 @@ oscar_status oscar_chunk_attend(oscar_pool* p, int32_t layer, const void* q, con
   cudaError_t e = cudaSuccess;
   if (c.single.n_seqs > 0) {
     int n = 0;
-    e = launch_chunk_single(p->P, p->dims, c.single, layer, q, k_new, v_new, ws + c.chunk_bytes, out, st, &n);
+    ChunkBranch branch;
+    e = chunk_branch(p, st, &branch);
+    if (e == cudaSuccess)
+      e = launch_chunk_single(p->P, p->dims, c.single, layer, q, k_new, v_new, ws + c.chunk_bytes, out, branch, st, &n);
     p->launch_count += n;
   }
   if (e == cudaSuccess && c.chunk) {
