@@ -35,6 +35,12 @@ def bf16_chunk_attend(q, k_pages, v_pages, page_table, lengths, cu_tokens, err, 
         out = torch.empty((n, hq, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
     else:
         _need(out, torch.bfloat16, (n, hq, HEAD_DIM), "out")
+    device = q.get_device()
+    for t in (k_pages, v_pages, page_table, lengths, cu_tokens, err, workspace, out):
+        if t.get_device() != device:
+            raise ValueError("pages, tables, workspace and out must be on the device of q")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     B._check("oscar_bf16_chunk", lib.oscar_bf16_chunk(
         hq, hkv, seqs, n, k_pages.data_ptr(), v_pages.data_ptr(), pages, page_table.data_ptr(), width, lengths.data_ptr(),
         cu_tokens.data_ptr(), q.data_ptr(), stride, workspace.data_ptr(), workspace.nbytes, out.data_ptr(), err.data_ptr(),
@@ -53,6 +59,6 @@ def bf16_copy_pages(k_pages, v_pages, src, dst):
     pages, hkv = shape[-4], shape[-3]
     _need(k_pages, torch.bfloat16, tuple(shape[:-2]) + (PAGE, HEAD_DIM), "k_pages")
     _need(v_pages, torch.bfloat16, tuple(shape), "v_pages")
-    if not _on_current_device(k_pages):
-        raise ValueError("k_pages must be on the current CUDA device")
+    if not _on_current_device(k_pages) or not _on_current_device(v_pages):
+        raise ValueError("k_pages and v_pages must be on the current CUDA device")
     B.oscar_bf16_copy_pages(hkv, layers, pages * hkv * PAGE * HEAD_DIM * 2, k_pages, v_pages, pages, src, dst, _raw_stream())

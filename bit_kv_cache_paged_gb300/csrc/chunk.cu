@@ -9,25 +9,40 @@
 //   O += P V     P [128 rows x 128 keys] from tensor memory, V [128 keys x 128] in shared memory
 // A tile's 128 rows are 128/hg tokens x the hg query heads of one KV head, so all of them share
 // every K and V block. A CTA works on two tiles at once: while one tile's 128 threads (a thread per
-// row) turn S into P, the tensor cores run the other tile's products. A tile costs 2 x 512 cycles of
-// tensor core per 128 keys and as many exponentials per row; both bound the long chunks.
+// row) turn S into P, the tensor cores run the other tile's products.
 //
 // Keys come in blocks of 128 (two half blocks of 64, each a page or a run of rows):
 //   pages of the BF16 cache, the pool's sink page and ring pages   tensor copies of a page's two 64-dim
 //       halves: the page's own swizzle (chunk c of token t at c ^ (t & 7)) is the 128-byte swizzle the
 //       tensor cores read, so a page is used as it lies
 //   the chunk's own rows (pool)       tensor copies with the 128-byte swizzle
-//   INT2 history (pool)               four warps turn the codes into fp16 tiles of the same layout
+//   INT2 history (pool)               as fp16 tiles of the same layout: four warps turn the codes into them
+//       (mode kDequant), or, where several pairs of tiles go over a history, chunk_tiles.cu has made them
+//       before and bulk copies bring them in (mode kTiles)
 // The INT2 blocks come first. For them Q is rotated on the tensor cores (Q R_K, R in two bf16 limbs)
 // and kept as fp16 with a power of two per row, k^ and v^ = fp16(level * s + z) and P are fp16, and
 // O is in the rotated basis: behind the last INT2 block it is split into two bf16 limbs and
 // multiplied by R_V^T in place (three products), and the BF16 blocks follow with the plain Q.
 //
-// Work: unit = one key block of one item (sequence, KV head, pair of tiles). The units of the whole
-// call are one range, cut into equal parts for the CTAs; an item cut by a boundary leaves one
+// Work: the key blocks of the items (sequence, KV head, pair of tiles), counted by what they cost. The
+// whole call is one range, cut into equal parts for the CTAs; an item cut by a boundary leaves one
 // partial (maximum, sum, unnormalised O) per part, and a second kernel joins them. This keeps every
 // SM busy for one long sequence with few rows as for a ragged batch, and needs nothing from the host:
 // lengths are read on the device, so a captured call follows them.
+//
+// What bounds it. 128 keys cost the two tiles 2048 cycles of products and take 2670: work issued ahead
+// keeps the tensor cores busy over gaps of 180 cycles only, a wait costs 60, and a tile's own chain (its
+// products, 1024; the softmax, 1240; the signals between them, 200) is longer than its turn. Not the
+// copies (half of their bytes left out change nothing) and not shared memory (products alone run at
+// their full rate beside them). Beside that an item costs 6000 cycles a tile for queries, masked blocks
+// and output. With codes dequantised in the kernel a block takes 3800 cycles, the expansion.
+// Measured (GB300, 32 query and 8 KV heads unless said; products counted for visible keys only):
+//   8192 new tokens                             362 us, 1520 TFLOP/s
+//   1024 new after 64K, 64 query heads          1490 to 1640 us, 1350 to 1490 TFLOP/s (the power limit's clock)
+//   12 sequences of 1 to 257 after up to 8K     142 us (up to 185 behind work that has drawn the clock down)
+//   16 sequences of 4 after 1K to 32K           182 us, 6420 GB/s: memory bound, the pages at 94% of the copy peak
+//   pool, 2048 new after 30000 of INT2          705 us, 1480 TFLOP/s, of it 21 us for the tiles
+//   pool, 10 of 1 to 300 after up to 6K, 64 query heads, group 32      285 us, of it 23 us for the tiles
 //
 // Keys no row may see, and what lies behind a sequence's last key, must not reach a sum even as 0 *
 // NaN: such values are zeroed in shared memory before the product. Where some rows of the tile see
@@ -904,39 +919,39 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MODE>* sh, uint8_t* sq, 
       bool fresh = __any_sync(0xffffffffu, m == -INFINITY);
       const float2 sc2 = make_float2(scale, scale);
       if constexpr (MODE == kDequant) {
-      bool again = fresh;
+        bool again = fresh;
 #pragma unroll 1
-      for (int c = 0;;) {
-        if (again) {
-          grow(c);
-          fresh = true;
-          again = false;
-        }
-        const float nm = m == -INFINITY ? 0.f : -m;
-        const float2 nm2 = make_float2(nm, nm);
-#pragma unroll 1
-        for (; c < 4; ++c) {
-          uint32_t x[32], p[16];
-          float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-          tc_ld32_issue(tS + 32 * c, x);
-          tc_ld_wait1(x);
-          // two scores an instruction, but for the exponentials
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc2, nm2);
-            e.x = fast_exp2(e.x);
-            e.y = fast_exp2(e.y);
-            if (i & 1) s1 = __fadd2_rn(s1, e); else s0 = __fadd2_rn(s0, e);
-            p[i] = pack2<decltype(half16)::value>(e.x, e.y);
+        for (int c = 0;;) {
+          if (again) {
+            grow(c);
+            fresh = true;
+            again = false;
           }
-          s0 = __fadd2_rn(s0, s1);
-          again = !fresh && __any_sync(0xffffffffu, s0.x + s0.y > kGrown);
-          if (again) break;
-          sum = __fadd2_rn(sum, s0);
-          tc_st16(tS + 16 * c, p);  // the columns of scores already read
+          const float nm = m == -INFINITY ? 0.f : -m;
+          const float2 nm2 = make_float2(nm, nm);
+#pragma unroll 1
+          for (; c < 4; ++c) {
+            uint32_t x[32], p[16];
+            float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+            tc_ld32_issue(tS + 32 * c, x);
+            tc_ld_wait1(x);
+            // two scores an instruction, but for the exponentials
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sc2, nm2);
+              e.x = fast_exp2(e.x);
+              e.y = fast_exp2(e.y);
+              if (i & 1) s1 = __fadd2_rn(s1, e); else s0 = __fadd2_rn(s0, e);
+              p[i] = pack2<decltype(half16)::value>(e.x, e.y);
+            }
+            s0 = __fadd2_rn(s0, s1);
+            again = !fresh && __any_sync(0xffffffffu, s0.x + s0.y > kGrown);
+            if (again) break;
+            sum = __fadd2_rn(sum, s0);
+            tc_st16(tS + 16 * c, p);  // the columns of scores already read
+          }
+          if (!again) break;
         }
-        if (!again) break;
-      }
       } else {
         uint32_t p[64];
         for (;; fresh = true) {
@@ -1061,47 +1076,47 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MODE>* sh, uint8_t* sq, 
       tc_ld32_issue(tO + 32 * c, o);
       tc_ld_wait1(o);
       if (live) {
-      float f[32];
+        float f[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]);
-      if (bad) {  // non-finite values this row does see
-        const int j0 = cur.keys_all() / kTile;
-        for (int b = 0; b < kTile * 4; ++b) {
-          const int key = j0 * kTile + b;
-          if (key >= lim || !((sh->bad[sb][b >> 7][(b >> 5) & 3] >> (b & 31)) & 1)) continue;
-          const __nv_bfloat16* v;
-          int swz = 0;
-          if constexpr (MODE != kBf16) {
-            v = C.v_new + ((int64_t)(cur.s.row0 + key) * C.Hkv + cur.h) * kHeadDim;
-          } else {
-            int64_t pid = C.page_table[(int64_t)cur.i * C.max_pages + (key >> 6)];
-            if (pid < 0 || pid >= C.n_pages_total) pid = 0;
-            v = reinterpret_cast<const __nv_bfloat16*>(C.v_pages) + (((int64_t)pid * C.Hkv + cur.h) * kPage + (key & 63)) * kHeadDim;
-            swz = key & 7;
-          }
+        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]);
+        if (bad) {  // non-finite values this row does see
+          const int j0 = cur.keys_all() / kTile;
+          for (int b = 0; b < kTile * 4; ++b) {
+            const int key = j0 * kTile + b;
+            if (key >= lim || !((sh->bad[sb][b >> 7][(b >> 5) & 3] >> (b & 31)) & 1)) continue;
+            const __nv_bfloat16* v;
+            int swz = 0;
+            if constexpr (MODE != kBf16) {
+              v = C.v_new + ((int64_t)(cur.s.row0 + key) * C.Hkv + cur.h) * kHeadDim;
+            } else {
+              int64_t pid = C.page_table[(int64_t)cur.i * C.max_pages + (key >> 6)];
+              if (pid < 0 || pid >= C.n_pages_total) pid = 0;
+              v = reinterpret_cast<const __nv_bfloat16*>(C.v_pages) + (((int64_t)pid * C.Hkv + cur.h) * kPage + (key & 63)) * kHeadDim;
+              swz = key & 7;
+            }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int d = 32 * c + i;
-            const float x = __bfloat162float(v[(((d >> 3) ^ swz) << 3) + (d & 7)]);
-            if (!isfinite(x)) f[i] += x;
+            for (int i = 0; i < 32; ++i) {
+              const int d = 32 * c + i;
+              const float x = __bfloat162float(v[(((d >> 3) ^ swz) << 3) + (d & 7)]);
+              if (!isfinite(x)) f[i] += x;
+            }
           }
         }
-      }
-      if (whole) {
+        if (whole) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t w[8];
+          for (int i = 0; i < 2; ++i) {
+            uint32_t w[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(f[16 * i + 2 * e] * inv, f[16 * i + 2 * e + 1] * inv);
-            w[e] = *reinterpret_cast<const uint32_t*>(&x);
+            for (int e = 0; e < 8; ++e) {
+              const __nv_bfloat162 x = __floats2bfloat162_rn(f[16 * i + 2 * e] * inv, f[16 * i + 2 * e + 1] * inv);
+              w[e] = *reinterpret_cast<const uint32_t*>(&x);
+            }
+            store32(dst + 32 * c + 16 * i, w, C.wide);
           }
-          store32(dst + 32 * c + 16 * i, w, C.wide);
-        }
-      } else {
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) store32(slot + 32 * c + 8 * i, reinterpret_cast<const uint32_t*>(f) + 8 * i, true);
-      }
+          for (int i = 0; i < 4; ++i) store32(slot + 32 * c + 8 * i, reinterpret_cast<const uint32_t*>(f) + 8 * i, true);
+        }
       }
       __syncwarp();  // the next tensor-memory load is the whole warp's
     }

@@ -155,6 +155,9 @@ class Pool:
             out = torch.empty_like(q)
         else:
             _need(out, torch.bfloat16, (T, self.Hq, HEAD_DIM), "out")
+        for t in (q, k_new, v_new, out):  # the pool's device must be current too, which the library checks
+            if not _on_current_device(t):
+                raise ValueError("q, k_new, v_new and out must be on the current CUDA device")
         # a buffer of the call's own: torch's allocator keeps it apart from calls on other streams
         # and from captured graphs
         lib = B.lib()

@@ -76,6 +76,8 @@ class Rope:
                     raise ValueError(f"k_out must have shape {tuple(k.shape)}, got {tuple(k_out.shape)}")
             kp, kop = k.data_ptr(), k_out.data_ptr()
         _need(positions, torch.int32, (n,), "positions")
+        if positions.get_device() != q.get_device():
+            raise ValueError("positions must be on the device of q")
         B._check("oscar_rope_apply", B.lib().oscar_rope_apply(self._ref, n, positions.data_ptr(), hq, q.data_ptr(), qs,
                                                               q_out.data_ptr(), qos, hk, kp, ks, kop, kos, _raw_stream()))
         return q_out, k_out

@@ -230,8 +230,10 @@ oscar_status oscar_step_graph(oscar_pool* pool, const void* k_new_bf16, const vo
  * it in INT2.
  *   q: dev bf16 [sum(n_new)][num_q_heads][128]; k_new, v_new: dev bf16 [sum(n_new)][num_kv_heads][128],
  *   rows as for oscar_append_and_demote; out: dev bf16, shape of q; workspace: dev scratch of
- *   oscar_chunk_workspace_bytes(pool) bytes (calls that may overlap need one each). All 16-byte aligned.
- * Runs on the pool's device, which must be current (OSCAR_EINVAL). Errors found by the kernels
+ *   oscar_chunk_workspace_bytes(pool) bytes, which depends on the step (calls that may overlap need one
+ *   each). All 16-byte aligned.
+ * One to seven launches, chosen on the host by the step's lengths: a captured call may be replayed for
+ * this step only. Runs on the pool's device, which must be current (OSCAR_EINVAL). Errors found by the kernels
  * (a bad page id, a bounded wait) surface from oscar_check. */
 size_t oscar_chunk_workspace_bytes(const oscar_pool* pool);
 oscar_status oscar_chunk_attend(oscar_pool* pool, int32_t layer, const void* q_bf16,

@@ -553,3 +553,51 @@ def test_pool_chunk_on_a_stream_and_in_graphs():
     torch.cuda.synchronize()
     assert torch.equal(got, want)
     m.pool.check()
+
+
+def test_pool_long_single_tokens_on_streams_and_in_graphs():
+    """The decode kernels' path runs on two branches outside a capture and on one inside; the outputs are the same bits."""
+    m = Mixed(hq=32, hkv=8, seed=15, max_seqs=8, max_len=4096)
+    ctx = [3900, 3000, 2500, 3900, 3500, 3333]
+    ids = list(range(len(ctx)))
+    for i in ids:
+        m.add(i)
+    m.pool.step_begin(ids, ctx)
+    kv = m.new_rows(sum(ctx))
+    m.pool.append_and_demote(0, kv[0][0], kv[1][0])
+    m.pool.step_begin(ids, [1] * len(ids))
+    kn, vn = (x[0] for x in m.new_rows(len(ids)))
+    q = torch.randn((len(ids), 32, E), generator=m.g, device="cuda").bfloat16()
+    launches = m.pool.launch_count()
+    want = m.pool.chunk_attend(0, q, kn, vn)
+    assert m.pool.launch_count() - launches > 4  # of them a chunk alone has at most four
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for k in range(12):
+        with torch.cuda.stream(streams[k % 3]):
+            got.append(m.pool.chunk_attend(0, q, kn, vn))
+    out = torch.empty_like(want)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        m.pool.chunk_attend(0, q, kn, vn, out=out)
+        m.pool.chunk_attend(0, q, kn, vn, out=out)
+    gr.replay()
+    gr.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in got + [out])
+    m.pool.check()
+
+
+def test_buffers_elsewhere_are_refused():
+    c = Pages([100], 2)
+    q = torch.randn((5, 8, E), device="cuda").bfloat16()
+    nb = B.oscar_bf16_chunk_workspace_bytes(8, 2, 1, 5)
+    with pytest.raises(ValueError):
+        c.attend(q, [5], workspace=torch.empty(nb, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        c.attend(q, [5], workspace=torch.empty(2 * nb, dtype=torch.uint8, device="cuda")[::2])
+    with pytest.raises(B.OscarError):
+        c.attend(q, [5], workspace=torch.empty(nb - 1, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        Rope().apply(q, None, torch.arange(5, dtype=torch.int32))
