@@ -601,3 +601,55 @@ def test_buffers_elsewhere_are_refused():
         c.attend(q, [5], workspace=torch.empty(nb - 1, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         Rope().apply(q, None, torch.arange(5, dtype=torch.int32))
+
+
+def test_bf16_many_sequences():
+    r = np.random.default_rng(5)
+    lens = r.integers(0, 200, 700).tolist()
+    new = [int(r.integers(0, min(n, 9) + 1)) for n in lens]
+    c = Pages(lens, 1, seed=31)
+    q = torch.randn((sum(new), 4, E), generator=torch.Generator(device="cuda").manual_seed(31), device="cuda").bfloat16()
+    c.check(q, new, c.attend(q, new))
+    assert int(c.err) == 0
+
+
+@pytest.mark.parametrize("most", [1, 4, 330])
+def test_pool_many_sequences(most):
+    """More sequences than a block has threads, on each of the paths: single tokens beside others, chunks, long chunks."""
+    n = 290
+    m = Mixed(hq=4, hkv=1, seed=32, max_seqs=n, max_len=1100)
+    r = np.random.default_rng(most)
+    ctx = r.integers(400, 700, n).tolist()
+    ids = r.permutation(n).tolist()
+    for i in range(n):
+        m.add(i)
+    m.pool.step_begin(ids, ctx)
+    kv = m.new_rows(sum(ctx))
+    m.pool.append_and_demote(0, kv[0][0], kv[1][0])
+    at = np.concatenate([[0], np.cumsum(ctx)])
+    for j, i in enumerate(ids):
+        m.rows[i] = [x[:, at[j]:at[j + 1]] for x in kv]
+    new = [1 if most == 1 and j % 5 else 300 if most == 330 and j % 3 else int(r.integers(0, most + 1)) for j in range(n)]
+    m.chunk(ids[::-1], new, append=False)
+
+
+def test_pool_bad_page_of_a_long_chunk_is_reported():
+    m = Mixed(hq=8, hkv=1, seed=33, max_seqs=2)
+    for i in (0, 1):
+        m.add(i)
+    m.chunk([0, 1], [900, 900])
+    st = torch.cuda.current_stream().cuda_stream
+    m.pool.step_begin([0, 1], [400, 300])
+    kn, vn = m.new_rows(700)
+    q = torch.randn((700, 8, E), generator=m.g, device="cuda").bfloat16()
+    good = m.pool.chunk_attend(0, q, kn[0], vn[0])
+    for bad in (-1, m.pool.cfg.max_int2_pages):
+        B.oscar_debug_set_page_entry(m.pool.handle, 1, 2, bad, st)
+        out = m.pool.chunk_attend(0, q, kn[0], vn[0])
+        with pytest.raises(B.OscarError) as e:
+            m.pool.check()
+        assert e.value.detail & B.DEVERR_PAGE
+        assert torch.equal(out[:400], good[:400])
+        B.oscar_debug_restore_page_table(m.pool.handle, 1, st)
+    assert torch.equal(m.pool.chunk_attend(0, q, kn[0], vn[0]), good)
+    m.pool.check()
