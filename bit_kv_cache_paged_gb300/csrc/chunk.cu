@@ -1265,50 +1265,47 @@ template <int MODE>
 __device__ int plan(const ChunkArgs& C, Shared<MODE>* sh, int64_t& g0, int64_t& g1) {
   constexpr int NT = kChunkThreads<MODE>, NW = NT / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // the first NT sequences stay in registers for the second pass
-  SeqWork s0{};
-  if (threadIdx.x < C.n_seqs) s0 = load_seq<MODE>(C, threadIdx.x);
-  const int64_t per0 = units_of(s0, C.lg);
-  int64_t mine = per0 * C.Hkv, total = 0;
-  for (int i = threadIdx.x + NT; i < C.n_seqs; i += NT) mine += units_of(load_seq<MODE>(C, i), C.lg) * C.Hkv;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sh->scan[warp] = mine;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < NW; ++w) total += sh->scan[w];
-  const int n = (int)min((int64_t)gridDim.x, max((int64_t)1, total / kMinUnits));
-  g0 = boundary(blockIdx.x, total, n);
-  g1 = boundary(blockIdx.x + 1, total, n);
-  if (g0 >= g1) return n;
-  if (threadIdx.x == 0) sh->total = total;
-  int64_t base = 0;
-  for (int i0 = 0; i0 < C.n_seqs; i0 += NT) {
-    const int i = i0 + threadIdx.x;
-    SeqWork s = s0;
-    int64_t per = per0;
-    if (i0) {
-      s = SeqWork{};
-      if (i < C.n_seqs) s = load_seq<MODE>(C, i);
-      per = units_of(s, C.lg);
-    }
-    const int64_t cnt = per * C.Hkv;
-    int64_t inc = cnt;
+  // The first NT sequences stay in registers; their scan is the only one of a call without more.
+  SeqWork s{};
+  if (threadIdx.x < C.n_seqs) s = load_seq<MODE>(C, threadIdx.x);
+  int64_t per = units_of(s, C.lg), inc, base, before;
+  auto scan = [&]() {  // units before this thread's sequence of the round, and behind the round
+    inc = per * C.Hkv;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    __syncthreads();
     if (lane == 31) sh->scan[warp] = inc;
     __syncthreads();
-    int64_t before = base + inc - cnt;
+    before = base + inc - per * C.Hkv;
+#pragma unroll
     for (int w = 0; w < NW; ++w) {
       const int64_t y = sh->scan[w];
       if (w < warp) before += y;
       base += y;
     }
-    if (cnt > 0 && g0 >= before && g0 < before + cnt) {
+  };
+  base = 0;
+  scan();
+  int64_t total = base;
+  if (C.n_seqs > NT) {
+    int64_t more = 0;
+    for (int i = threadIdx.x + NT; i < C.n_seqs; i += NT) more += units_of(load_seq<MODE>(C, i), C.lg) * C.Hkv;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) more += __shfl_xor_sync(0xffffffffu, more, o);
+    __syncthreads();
+    if (lane == 0) sh->scan[warp] = more;
+    __syncthreads();
+    for (int w = 0; w < NW; ++w) total += sh->scan[w];
+  }
+  const int n = (int)min((int64_t)gridDim.x, max((int64_t)1, total / kMinUnits));
+  g0 = boundary(blockIdx.x, total, n);
+  g1 = boundary(blockIdx.x + 1, total, n);
+  if (g0 >= g1) return n;
+  if (threadIdx.x == 0) sh->total = total;
+  for (int i = threadIdx.x;; i += NT) {
+    if (per > 0 && g0 >= before && g0 < before + per * C.Hkv) {
       int64_t x = g0 - before;
       int h = 0;
       while (x >= per) {
@@ -1326,6 +1323,11 @@ __device__ int plan(const ChunkArgs& C, Shared<MODE>* sh, int64_t& g0, int64_t& 
       sh->st_x = x - units_before(s, C.lg, lo);
     }
     if (base > g0) break;
+    s = SeqWork{};
+    if (i + NT < C.n_seqs) s = load_seq<MODE>(C, i + NT);
+    per = units_of(s, C.lg);
+    __syncthreads();  // the last round's sums have been read
+    scan();
   }
   return n;
 }
@@ -1359,6 +1361,7 @@ __global__ void __launch_bounds__(kChunkThreads<MODE>, 1)
     sh->abort = 0;
     fence_mbar_init();
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may come up; it waits for this grid's end
   int64_t g0, g1;
   const int n = plan<MODE>(C, sh, g0, g1);
   if (threadIdx.x == 0 && g0 >= g1) reinterpret_cast<Part*>(C.ws)[blockIdx.x].parts = 0;
@@ -1441,6 +1444,7 @@ __global__ void __launch_bounds__(kChunkThreads<MODE>, 1)
 // 64 tokens after 500 is 7 us longer (21 us).
 constexpr int kJoinEach = 2, kJoinDepth = 2, kJoinRows = 8 * kJoinEach;
 __global__ void __launch_bounds__(256) k_chunk_join(const __grid_constant__ ChunkArgs C) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while k_chunk still runs
   const Part d = reinterpret_cast<const Part*>(C.ws)[blockIdx.x];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row0 = blockIdx.y * kJoinRows + warp;
@@ -1563,8 +1567,17 @@ cudaError_t launch_chunk(const ChunkArgs& C, const ChunkMaps& M, cudaStream_t s)
   k_chunk<MODE><<<ctas, kChunkThreads<MODE>, kChunkSmem<MODE>, s>>>(C, M);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
-  k_chunk_join<<<dim3(ctas, C.rows / kJoinRows), 256, 0, s>>>(C);
-  return cudaGetLastError();
+  // its launch overlaps the end of k_chunk
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t join{};
+  join.gridDim = dim3(ctas, C.rows / kJoinRows);
+  join.blockDim = dim3(256);
+  join.stream = s;
+  join.attrs = &early;
+  join.numAttrs = 1;
+  return cudaLaunchKernelEx(&join, k_chunk_join, C);
 }
 
 }  // namespace
