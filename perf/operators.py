@@ -186,7 +186,7 @@ def prepare(case, seed):
         if own:
             from bit_kv_cache_paged_gb300 import Rope
             st["rope"] = Rope(rot_dim=case["rot"], interleaved=case["inter"], base=case["base"], scaling=case["scaling"],
-                              factor=case["factor"], original_len=32768)
+                              factor=case["factor"] if case["scaling"] != "none" else 1.0, original_len=32768)
         return st
     if op == "copy":
         shape = (case["layers"], case["pages"], case["hkv"], PAGE, E)
