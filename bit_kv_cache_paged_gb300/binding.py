@@ -6,6 +6,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+from array import array
 
 from .build import LIB, ROOT
 
@@ -77,8 +78,7 @@ _SIGS = {
     "oscar_bf16_chunk_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32, c_i32]),
     "oscar_bf16_chunk": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_i64, c_vp, c_i32, c_vp, c_vp, c_vp, c_i64,
                                  c_vp, c_sz, c_vp, c_vp, c_vp]),
-    "oscar_bf16_copy_pages": (c_i32, [c_i32, c_i32, c_sz, c_vp, c_vp, c_i64, ctypes.POINTER(c_i32),
-                                      ctypes.POINTER(c_i32), c_i32, c_vp]),
+    "oscar_bf16_copy_pages": (c_i32, [c_i32, c_i32, c_sz, c_vp, c_vp, c_i64, c_vp, c_vp, c_i32, c_vp]),
     "oscar_rope_init": (c_i32, [ctypes.POINTER(OscarRopeConfig), ctypes.POINTER(OscarRope)]),
     "oscar_rope_apply": (c_i32, [ctypes.POINTER(OscarRope), c_i32, c_vp, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp,
                                  c_i64, c_vp, c_i64, c_vp]),
@@ -245,13 +245,12 @@ def oscar_bf16_chunk(num_q_heads, num_kv_heads, n_seqs, n_tokens, k_pages, v_pag
 
 def oscar_bf16_copy_pages(num_kv_heads, n_layers, layer_stride, k_pages, v_pages, n_pages_total, src, dst, stream):
     """src, dst: host sequences of page ids (pairs)."""
-    if len(src) != len(dst):
-        raise OscarError("oscar_bf16_copy_pages", OSCAR_EINVAL)
     n = len(src)
-    a = (c_i32 * n)(*[int(x) for x in src])
-    b = (c_i32 * n)(*[int(x) for x in dst])
-    _check("oscar_bf16_copy_pages", lib().oscar_bf16_copy_pages(num_kv_heads, n_layers, layer_stride, _ptr(k_pages),
-                                                                _ptr(v_pages), n_pages_total, a, b, n, stream))
+    if n != len(dst):
+        raise OscarError("oscar_bf16_copy_pages", OSCAR_EINVAL)
+    a, b = array("i", src), array("i", dst)  # int32; ids that do not fit raise OverflowError
+    _check("oscar_bf16_copy_pages", lib().oscar_bf16_copy_pages(num_kv_heads, n_layers, layer_stride, _ptr(k_pages), _ptr(v_pages),
+                                                                n_pages_total, a.buffer_info()[0], b.buffer_info()[0], n, stream))
 
 
 def oscar_rope_init(cfg: OscarRopeConfig) -> OscarRope:
