@@ -75,8 +75,10 @@ constexpr float kGrown = 16384.f;             // a block's weights under an old 
 constexpr int kDescBytes = 32;
 // Work is counted in thousands of SM cycles, as measured on batches of equal items (G = 128, hg = 4):
 // a block of BF16 keys takes 3, one of INT2 keys 4; an item takes another 6 a tile (queries in, first
-// and masked blocks, output out), and 8 more a tile for its two rotations.
-constexpr int kUnitsBf16 = 3, kUnitsInt2 = 4, kUnitsTile = 6, kUnitsRotate = 8;
+// and masked blocks, output out), and 8 more a tile for its two rotations. Where the fp16 tiles are made
+// beforehand the rotations weigh twice as much beside the faster blocks: with 16 the ragged batch of 10
+// takes 259 us for 282 with 8, others 0.93 to 1.01 of the time (24 gives 260, and 0.94 to 1.08).
+constexpr int kUnitsBf16 = 3, kUnitsInt2 = 4, kUnitsTile = 6, kUnitsRotate = 8, kUnitsRotateTiles = 16;
 constexpr int kMinUnits = 4;  // per CTA, at least: a block and a little (64 tokens after 500: 28 us at 12, 20 at 3 to 6)
 
 constexpr uint32_t kIdescBase = (1u << 4) | ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
@@ -126,6 +128,7 @@ struct SeqWork {
   int32_t nI, nB;                 // INT2 blocks, blocks of cached BF16 pages (pool)
   int32_t hist, F, L, sink, seq;  // pool: history tokens, frontier and length before the step
   int32_t tile0;                  // first block of its tiles
+  int32_t rotate;                 // units of a tile's two rotations
 };
 
 template <int MODE>
@@ -147,6 +150,7 @@ __device__ __forceinline__ SeqWork load_seq(const ChunkArgs& C, int i) {
     s.nB = s.L > 0 ? (1 + ring + 1) / 2 : 0;
     s.A = 0;
     if (MODE == kTiles) s.tile0 = C.tile_base[i];
+    s.rotate = s.nI <= 0 ? 0 : MODE == kTiles ? kUnitsRotateTiles : kUnitsRotate;
   } else {
     const int a = min(max(C.cu[i], 0), C.n_tokens), b = min(max(C.cu[i + 1], a), C.n_tokens);
     int len = max(C.lengths[i], 0);
@@ -169,7 +173,7 @@ __device__ __forceinline__ int real_blocks(const SeqWork& s, int lg, int t) {
 
 __device__ __forceinline__ int pairs_of(const SeqWork& s, int lg) { return (s.n + (1 << lg) - 1) >> lg; }
 __device__ __forceinline__ int item_overhead(const SeqWork& s, int tiles) {
-  return tiles * (kUnitsTile + (s.nI > 0 ? kUnitsRotate : 0));
+  return tiles * (kUnitsTile + s.rotate);
 }
 __device__ __forceinline__ int item_tiles(const SeqWork& s, int lg, int t) { return s.n - (t << lg) > (1 << lg) / 2 ? 2 : 1; }
 // Units of an item of nb blocks (an item without keys counts one).
