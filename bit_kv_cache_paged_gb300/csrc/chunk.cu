@@ -39,10 +39,10 @@
 // Measured (GB300, 32 query and 8 KV heads unless said; products counted for visible keys only):
 //   8192 new tokens                             362 us, 1520 TFLOP/s
 //   1024 new after 64K, 64 query heads          1490 to 1640 us, 1350 to 1490 TFLOP/s (the power limit's clock)
-//   12 sequences of 1 to 257 after up to 8K     142 us (up to 185 behind work that has drawn the clock down)
+//   12 sequences of 1 to 257 after up to 8K     144 us (up to 185 behind work that has drawn the clock down)
 //   16 sequences of 4 after 1K to 32K           182 us, 6420 GB/s: memory bound, the pages at 94% of the copy peak
 //   pool, 2048 new after 30000 of INT2          705 us, 1480 TFLOP/s, of it 21 us for the tiles
-//   pool, 10 of 1 to 300 after up to 6K, 64 query heads, group 32      285 us, of it 23 us for the tiles
+//   pool, 10 of 1 to 300 after up to 6K, 64 query heads, group 32      256 us, of it 23 us for the tiles
 //
 // Keys no row may see, and what lies behind a sequence's last key, must not reach a sum even as 0 *
 // NaN: such values are zeroed in shared memory before the product. Where some rows of the tile see
