@@ -1654,7 +1654,7 @@ oscar_status oscar_bf16_chunk(int32_t num_q_heads, int32_t num_kv_heads, int32_t
   if (q_token_stride % 8 || q_token_stride < (int64_t)num_q_heads * kHeadDim || q_token_stride >= (1ll << 38)) return OSCAR_EINVAL;
   // rows of the page buffers are addressed by 31-bit coordinates (549 GB of K)
   if (workspace_bytes < need || n_pages_total < 1 || n_pages_total > INT32_MAX / kPage / num_kv_heads || max_pages_per_seq < 1 ||
-      max_pages_per_seq > INT32_MAX / kPage)
+      max_pages_per_seq > (INT32_MAX - 4096) / kPage)  // positions and a few tiles beyond them are 32-bit
     return OSCAR_EINVAL;
   ChunkArgs C{};
   C.Hq = num_q_heads;

@@ -231,7 +231,7 @@ oscar_status oscar_step_graph(oscar_pool* pool, const void* k_new_bf16, const vo
  *   q: dev bf16 [sum(n_new)][num_q_heads][128]; k_new, v_new: dev bf16 [sum(n_new)][num_kv_heads][128],
  *   rows as for oscar_append_and_demote; out: dev bf16, shape of q; workspace: dev scratch of
  *   oscar_chunk_workspace_bytes(pool) bytes, which depends on the step (calls that may overlap need one
- *   each). All 16-byte aligned.
+ *   each). All 16-byte aligned; out may not overlap the inputs.
  * One to seven launches, chosen on the host by the step's lengths: a captured call may be replayed for
  * this step only. Runs on the pool's device, which must be current (OSCAR_EINVAL). Errors found by the kernels
  * (a bad page id, a bounded wait) surface from oscar_check. */
@@ -353,6 +353,7 @@ oscar_status oscar_bf16_decode(int32_t num_q_heads, int32_t num_kv_heads, int32_
  *     outputs are not valid; nothing outside the buffers is read or written).
  *   workspace: dev scratch of oscar_bf16_chunk_workspace_bytes(...) bytes, 16-byte aligned; calls
  *     that may overlap in time need one each.
+ *   out may not overlap q, the pages or the workspace.
  * Scores, softmax statistics and sums are fp32; the softmax weights enter the value product in
  * bf16. Asynchronous on `stream`; allocates nothing. */
 size_t oscar_bf16_chunk_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t n_seqs,

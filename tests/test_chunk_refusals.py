@@ -144,3 +144,15 @@ def test_pool_chunk_refused_outside_a_device_step():
 
 def test_structures_match_the_header():
     assert ctypes.sizeof(B.OscarRope) == 16 + 64 * 8 and ctypes.sizeof(B.OscarRopeConfig) == 16 + 5 * 8
+
+
+def test_bf16_chunk_positions_stay_in_32_bits():
+    nb = B.oscar_bf16_chunk_workspace_bytes(8, 2, 3, 100)
+    for width in ((2 ** 31 - 1 - 4096) // 64 + 1, 2 ** 25):
+        refused(B.oscar_bf16_chunk, 8, 2, 3, 100, A, A, 50, A, width, A, A, A, 1024, A, nb, A, A, None)
+
+
+def test_copy_pages_ids_past_32_bits():
+    for src, dst in (([2 ** 32 + 1], [2]), ([1], [2 ** 31])):
+        with pytest.raises(OverflowError):
+            B.oscar_bf16_copy_pages(2, 1, 0, A, 2 * A, 10, src, dst, None)
