@@ -40,7 +40,7 @@
 //   8192 new tokens                             362 us, 1520 TFLOP/s
 //   1024 new after 64K, 64 query heads          1490 to 1640 us, 1350 to 1490 TFLOP/s (the power limit's clock)
 //   12 sequences of 1 to 257 after up to 8K     144 us (up to 185 behind work that has drawn the clock down)
-//   16 sequences of 4 after 1K to 32K           182 us, 6420 GB/s: memory bound, the pages at 94% of the copy peak
+//   16 sequences of 4 after 1K to 32K           177 us, 6620 GB/s: memory bound, 97% of the copy peak
 //   pool, 2048 new after 30000 of INT2          705 us, 1480 TFLOP/s, of it 21 us for the tiles
 //   pool, 10 of 1 to 300 after up to 6K, 64 query heads, group 32      256 us, of it 23 us for the tiles
 //
@@ -393,6 +393,9 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MODE>* 
                           Cursor<MODE> cur) {
   // one lane
   const uint64_t keep = policy_evict_last(), once = policy_evict_first();
+  // Of the keys and values: kept in L2 where several pairs of tiles come for them (1K after 64K: 1590 us, 1640
+  // without), else let go (16 sequences of 4: 177 us for 182).
+  uint64_t policy = keep;
   Ring<MODE> r;
   uint32_t issued = 0, qn = 0;  // bit s: stage s has had a tensor copy
   uint32_t last_parity = 0;
@@ -443,7 +446,7 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MODE>* 
       uint64_t* bar;
       if (!stage(dst, bar)) return false;
       mbar_expect_tx(bar, kTileBytes);
-      bulk_g2s(dst, src + kv * kTileBytes, kTileBytes, bar, keep);
+      bulk_g2s(dst, src + kv * kTileBytes, kTileBytes, bar, policy);
     }
     return true;
   };
@@ -466,7 +469,7 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MODE>* 
       }
       bulk_g2s(codes + (size_t)(slot * 2 + x) * C.P.block_bytes,
                C.P.int2 + (size_t)C.layer * C.P.int2_layer_stride + ((size_t)pid[x] * C.Hkv + cur.h) * C.P.block_bytes,
-               C.P.block_bytes, &sh->code_full[slot], keep);
+               C.P.block_bytes, &sh->code_full[slot], policy);
     }
     ++cpos;
     return true;
@@ -520,9 +523,9 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MODE>* 
         for (int d = 0; d < 2; ++d) {
           uint8_t* to = dst + d * kHalfBytes + x * kPageHalfBytes;
           if (MODE != kBf16 && rows3)
-            tma_load_3d(to, map[x][kv], d * 64, cur.h, row[x], bar, keep);
+            tma_load_3d(to, map[x][kv], d * 64, cur.h, row[x], bar, policy);
           else
-            tma_load_2d(to, map[x][kv], d * 64, row[x], bar, keep);
+            tma_load_2d(to, map[x][kv], d * 64, row[x], bar, policy);
         }
       }
     }
@@ -531,6 +534,7 @@ __device__ void load_role(const ChunkArgs& C, const ChunkMaps& M, Shared<MODE>* 
   for (; ok && cur.valid(); cur.next(C)) {
     if (cur.empty()) continue;
     const int nI = MODE != kBf16 ? min(cur.k1, cur.s.nI) : 0;
+    policy = pairs_of(cur.s, cur.lg) > 1 ? keep : once;
     if (cur.k0 < nI) {
       ok = load_q() && load_limbs(0);
       if constexpr (MODE == kDequant) {
