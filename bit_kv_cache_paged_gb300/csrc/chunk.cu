@@ -898,6 +898,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MODE>* sh, uint8_t* sq, 
         l *= alpha;
         sum.x *= alpha;
         sum.y *= alpha;
+        if (c0 > 0) tc_st_wait();  // the weights read back below were stored without a wait
 #pragma unroll 1
         for (int c = 0; c < c0; ++c) {
           uint32_t w[16];
