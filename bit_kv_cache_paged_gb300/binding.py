@@ -74,7 +74,7 @@ _SIGS = {
     "oscar_bf16_decode": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_i64, c_vp, c_i32, c_vp, c_vp, c_vp,
                                   c_sz, c_vp, c_vp, c_vp]),
     "oscar_chunk_workspace_bytes": (c_sz, [c_vp]),
-    "oscar_chunk_attend": (c_i32, [c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "oscar_chunk_attend": (c_i32, [c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
     "oscar_bf16_chunk_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32, c_i32]),
     "oscar_bf16_chunk": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_i64, c_vp, c_i32, c_vp, c_vp, c_vp, c_i64,
                                  c_vp, c_sz, c_vp, c_vp, c_vp]),
@@ -270,9 +270,12 @@ def oscar_chunk_workspace_bytes(pool) -> int:
     return lib().oscar_chunk_workspace_bytes(pool)
 
 
-def oscar_chunk_attend(pool, layer, q, k_new, v_new, workspace, out, stream):
+def oscar_chunk_attend(pool, layer, q, k_new, v_new, workspace, out, stream, workspace_bytes=None):
+    """workspace_bytes None: the tensor's own size (an address has none, and is refused without it)."""
+    if workspace_bytes is None:
+        workspace_bytes = getattr(workspace, "nbytes", 0)
     _check("oscar_chunk_attend", lib().oscar_chunk_attend(pool, layer, _ptr(q), _ptr(k_new), _ptr(v_new),
-                                                          _ptr(workspace), _ptr(out), stream))
+                                                          _ptr(workspace), workspace_bytes, _ptr(out), stream))
 
 
 def oscar_partials_bytes(pool, n_seqs) -> int:

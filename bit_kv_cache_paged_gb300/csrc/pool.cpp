@@ -689,10 +689,13 @@ static ChunkPlan chunk_plan(const oscar_pool* p) {
   return c;
 }
 
+static size_t chunk_bytes(const ChunkPlan& c) {  // one more kAlign: the buffer may start anywhere
+  return c.chunk_bytes + c.single_bytes + c.tiles_bytes + kAlign;
+}
+
 size_t oscar_chunk_workspace_bytes(const oscar_pool* p) {
   if (!p || !p->in_step || p->host_only) return 0;
-  const ChunkPlan c = chunk_plan(p);
-  return c.chunk_bytes + c.single_bytes + c.tiles_bytes + kAlign;
+  return chunk_bytes(chunk_plan(p));
 }
 
 // The branch for a call on st. None under capture: a stream that has joined a capture belongs to it until it
@@ -710,7 +713,7 @@ static cudaError_t chunk_branch(oscar_pool* p, cudaStream_t st, ChunkBranch* out
 }
 
 oscar_status oscar_chunk_attend(oscar_pool* p, int32_t layer, const void* q, const void* k_new, const void* v_new,
-                                void* workspace, void* out, void* stream) {
+                                void* workspace, size_t workspace_bytes, void* out, void* stream) {
   if (!p || layer < 0 || layer >= p->cfg.num_layers) return OSCAR_EINVAL;
   if (!p->in_step) return OSCAR_ESTATE;
   if (p->host_only) return OSCAR_EINVAL;
@@ -722,6 +725,7 @@ oscar_status oscar_chunk_attend(oscar_pool* p, int32_t layer, const void* q, con
   if (cudaGetDevice(&dev) != cudaSuccess) return cuda_fail(cudaErrorUnknown);
   if (dev != p->device) return OSCAR_EINVAL;
   const ChunkPlan c = chunk_plan(p);
+  if (workspace_bytes < chunk_bytes(c)) return OSCAR_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<uintptr_t>(workspace)));
   cudaError_t e = cudaSuccess;

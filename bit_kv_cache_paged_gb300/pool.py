@@ -163,7 +163,7 @@ class Pool:
         lib = B.lib()
         workspace = torch.empty(max(lib.oscar_chunk_workspace_bytes(self.handle), 16), dtype=torch.uint8, device=q.device)
         B._check("oscar_chunk_attend", lib.oscar_chunk_attend(self.handle, layer, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
-                                                              workspace.data_ptr(), out.data_ptr(), _raw_stream()))
+                                                              workspace.data_ptr(), workspace.nbytes, out.data_ptr(), _raw_stream()))
         return out
 
     def step_graph(self, k_new, v_new, q, q_rot=None, out=None):

@@ -230,15 +230,16 @@ oscar_status oscar_step_graph(oscar_pool* pool, const void* k_new_bf16, const vo
  * it in INT2.
  *   q: dev bf16 [sum(n_new)][num_q_heads][128]; k_new, v_new: dev bf16 [sum(n_new)][num_kv_heads][128],
  *   rows as for oscar_append_and_demote; out: dev bf16, shape of q; workspace: dev scratch of
- *   oscar_chunk_workspace_bytes(pool) bytes, which depends on the step (calls that may overlap need one
- *   each). All 16-byte aligned; out may not overlap the inputs.
+ *   oscar_chunk_workspace_bytes(pool) bytes, which depends on the step: a buffer with fewer is refused
+ *   (OSCAR_EINVAL, nothing is launched). Calls that may overlap need one each. All 16-byte aligned; out
+ *   may not overlap the inputs.
  * One to seven launches, chosen on the host by the step's lengths: a captured call may be replayed for
  * this step only. Runs on the pool's device, which must be current (OSCAR_EINVAL). Errors found by the kernels
  * (a bad page id, a bounded wait) surface from oscar_check. */
 size_t oscar_chunk_workspace_bytes(const oscar_pool* pool);
 oscar_status oscar_chunk_attend(oscar_pool* pool, int32_t layer, const void* q_bf16,
                                 const void* k_new_bf16, const void* v_new_bf16, void* workspace,
-                                void* out_bf16, void* stream);
+                                size_t workspace_bytes, void* out_bf16, void* stream);
 
 /* Bytes of partials scratch that oscar_decode needs for the current step (n_seqs must equal the
  * step's batch): a bound that depends only on the batch size and the pool, so one buffer serves
