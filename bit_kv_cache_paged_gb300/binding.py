@@ -74,6 +74,7 @@ _SIGS = {
     "oscar_bf16_decode": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_i64, c_vp, c_i32, c_vp, c_vp, c_vp,
                                   c_sz, c_vp, c_vp, c_vp]),
     "oscar_chunk_workspace_bytes": (c_sz, [c_vp]),
+    "oscar_chunk_workspace_min_bytes": (c_sz, [c_vp]),
     "oscar_chunk_attend": (c_i32, [c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
     "oscar_bf16_chunk_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32, c_i32]),
     "oscar_bf16_chunk": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_i64, c_vp, c_i32, c_vp, c_vp, c_vp, c_i64,
@@ -268,6 +269,10 @@ def oscar_rope_apply(rope, n_tokens, positions, num_q_heads, q, q_stride, q_out,
 
 def oscar_chunk_workspace_bytes(pool) -> int:
     return lib().oscar_chunk_workspace_bytes(pool)
+
+
+def oscar_chunk_workspace_min_bytes(pool) -> int:
+    return lib().oscar_chunk_workspace_min_bytes(pool)
 
 
 def oscar_chunk_attend(pool, layer, q, k_new, v_new, workspace, out, stream, workspace_bytes=None):

@@ -650,6 +650,10 @@ struct ChunkPlan {
   bool chunk;       // rows for the chunk kernel
   int64_t tiles;    // blocks of 128 history tokens made into fp16 tiles for it (0: it dequantises itself)
   size_t chunk_bytes, single_bytes, tiles_bytes;
+  void drop_tiles() {
+    tiles = 0;
+    tiles_bytes = 0;
+  }
 };
 
 static ChunkPlan chunk_plan(const oscar_pool* p) {
@@ -698,6 +702,13 @@ size_t oscar_chunk_workspace_bytes(const oscar_pool* p) {
   return chunk_bytes(chunk_plan(p));
 }
 
+size_t oscar_chunk_workspace_min_bytes(const oscar_pool* p) {
+  if (!p || !p->in_step || p->host_only) return 0;
+  ChunkPlan c = chunk_plan(p);
+  c.drop_tiles();
+  return chunk_bytes(c);
+}
+
 // The branch for a call on st. None under capture: a stream that has joined a capture belongs to it until it
 // ends, and calls on other streams come here meanwhile.
 static cudaError_t chunk_branch(oscar_pool* p, cudaStream_t st, ChunkBranch* out) {
@@ -724,7 +735,8 @@ oscar_status oscar_chunk_attend(oscar_pool* p, int32_t layer, const void* q, con
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return cuda_fail(cudaErrorUnknown);
   if (dev != p->device) return OSCAR_EINVAL;
-  const ChunkPlan c = chunk_plan(p);
+  ChunkPlan c = chunk_plan(p);
+  if (workspace_bytes < chunk_bytes(c)) c.drop_tiles();
   if (workspace_bytes < chunk_bytes(c)) return OSCAR_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<uintptr_t>(workspace)));

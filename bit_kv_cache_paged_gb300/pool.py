@@ -143,10 +143,12 @@ class Pool:
         part = self.decode(layer, q, q_rot)
         return self.merge(layer, part)
 
-    def chunk_attend(self, layer, q, k_new, v_new, out=None):
+    def chunk_attend(self, layer, q, k_new, v_new, out=None, workspace=None):
         """Attention of the step's new tokens (bf16 q [Σn_new, Hq, 128], k_new / v_new [Σn_new, Hkv, 128]) over the
         cache as it stood before the step and the chunk itself, causal; between step_begin and this layer's
-        append_and_demote. Returns bf16 [Σn_new, Hq, 128]."""
+        append_and_demote. Returns bf16 [Σn_new, Hq, 128]. workspace: a contiguous uint8 tensor of at least
+        oscar_chunk_workspace_min_bytes (scratch of the call's own when None: as much as the call can use, or, where
+        that much is not free, the least)."""
         T = self.total_new
         _need(q, torch.bfloat16, (T, self.Hq, HEAD_DIM), "q")
         _need(k_new, torch.bfloat16, (T, self.Hkv, HEAD_DIM), "k_new")
@@ -158,10 +160,18 @@ class Pool:
         for t in (q, k_new, v_new, out):  # the pool's device must be current too, which the library checks
             if not _on_current_device(t):
                 raise ValueError("q, k_new, v_new and out must be on the current CUDA device")
-        # a buffer of the call's own: torch's allocator keeps it apart from calls on other streams
-        # and from captured graphs
         lib = B.lib()
-        workspace = torch.empty(max(lib.oscar_chunk_workspace_bytes(self.handle), 16), dtype=torch.uint8, device=q.device)
+        if workspace is None:
+            # a buffer of the call's own: torch's allocator keeps it apart from calls on other streams
+            # and from captured graphs
+            try:
+                workspace = torch.empty(max(lib.oscar_chunk_workspace_bytes(self.handle), 16), dtype=torch.uint8, device=q.device)
+            except torch.cuda.OutOfMemoryError:
+                workspace = torch.empty(max(lib.oscar_chunk_workspace_min_bytes(self.handle), 16), dtype=torch.uint8, device=q.device)
+        else:
+            _need(workspace, torch.uint8, workspace.shape, "workspace")
+            if not _on_current_device(workspace):
+                raise ValueError("workspace must be on the current CUDA device")
         B._check("oscar_chunk_attend", lib.oscar_chunk_attend(self.handle, layer, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
                                                               workspace.data_ptr(), workspace.nbytes, out.data_ptr(), _raw_stream()))
         return out

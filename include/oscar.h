@@ -230,13 +230,16 @@ oscar_status oscar_step_graph(oscar_pool* pool, const void* k_new_bf16, const vo
  * it in INT2.
  *   q: dev bf16 [sum(n_new)][num_q_heads][128]; k_new, v_new: dev bf16 [sum(n_new)][num_kv_heads][128],
  *   rows as for oscar_append_and_demote; out: dev bf16, shape of q; workspace: dev scratch of
- *   oscar_chunk_workspace_bytes(pool) bytes, which depends on the step: a buffer with fewer is refused
- *   (OSCAR_EINVAL, nothing is launched). Calls that may overlap need one each. All 16-byte aligned; out
- *   may not overlap the inputs.
+ *   workspace_bytes bytes, how many depends on the step. oscar_chunk_workspace_bytes(pool) includes room for
+ *   long histories as fp16 tiles (up to 4 GB); with less the codes are expanded in the kernel
+ *   (slower; sums in another order), down to oscar_chunk_workspace_min_bytes(pool), some 40 MB and the
+ *   decode partials of single tokens. A smaller buffer is refused (OSCAR_EINVAL, nothing is launched).
+ *   Calls that may overlap need one each. All 16-byte aligned; out may not overlap the inputs.
  * One to seven launches, chosen on the host by the step's lengths: a captured call may be replayed for
  * this step only. Runs on the pool's device, which must be current (OSCAR_EINVAL). Errors found by the kernels
  * (a bad page id, a bounded wait) surface from oscar_check. */
 size_t oscar_chunk_workspace_bytes(const oscar_pool* pool);
+size_t oscar_chunk_workspace_min_bytes(const oscar_pool* pool);
 oscar_status oscar_chunk_attend(oscar_pool* pool, int32_t layer, const void* q_bf16,
                                 const void* k_new_bf16, const void* v_new_bf16, void* workspace,
                                 size_t workspace_bytes, void* out_bf16, void* stream);
