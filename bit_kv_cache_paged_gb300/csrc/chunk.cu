@@ -71,7 +71,12 @@ constexpr int kCodeBuf = 3 * 2 * int2_block_bytes(128);  // packed INT2 pages in
 constexpr int kMaxSlots = 3;
 constexpr int kMaxCtas = 152;
 constexpr int kPageHalfBytes = kPage * 128;   // 64 dims of one page
-constexpr float kGrown = 16384.f;             // a block's weights under an old maximum: fp16 holds each of them
+constexpr float kGrown = 60000.f;             // a block's weights under an old maximum: fp16 holds each of them
+// The reference of INT2 scores is set 4 (in powers of two) below their maximum: the largest weight is 2^4, fp16 weights keep their 11
+// bits down to 2^-18 of it and are off by 2^-29 of it at most below that, half a step of a bf16 output for 2^20 such keys. With the
+// largest at 1 they vanish at 2^-25: 0.3% of the output for a flat history of 130 thousand tokens under one strong key. More
+// headroom means more renewals: 2048 after 30000 takes 768 us a call with 4, 771 with 5, 790 with 8 (766 with 0).
+constexpr float kHeadroom = 4.f;
 constexpr int kDescBytes = 32;
 // Work is counted in thousands of SM cycles, as measured on batches of equal items (G = 128, hg = 4):
 // a block of BF16 keys takes 3, one of INT2 keys 4; an item takes another 6 a tile (queries in, first
@@ -875,7 +880,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MODE>* sh, uint8_t* sq, 
         }
       }
       // The maximum is taken anew only where it must be: for the rows' first block, and when the weights of
-      // 32 scores under the last one sum to more than kGrown (each is finite then, or their sum infinite).
+      // 32 (or 128) scores under the last one sum to more than kGrown (each is finite then, or their sum infinite).
       // The weights already made are scaled then, as the sums and O are. The loops stay rolled: the warps'
       // instructions come from one cache, and unrolled they waited for it longer than for their data.
       float2 sum = make_float2(0.f, 0.f);
@@ -892,7 +897,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MODE>* sh, uint8_t* sq, 
             mx1 = max3(mx1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
           }
         }
-        const float mb = fmaxf(mx0, mx1) * scale;
+        const float mb = fmaxf(mx0, mx1) * scale - (decltype(half16)::value ? kHeadroom : 0.f);
         const float mn = fmaxf(m, mb), alpha = mb > m ? fast_exp2(m - mn) : 1.f;
         m = mn;
         l *= alpha;
