@@ -235,7 +235,8 @@ oscar_status oscar_step_graph(oscar_pool* pool, const void* k_new_bf16, const vo
  *   (slower; sums in another order), down to oscar_chunk_workspace_min_bytes(pool), some 40 MB and the
  *   decode partials of single tokens. A smaller buffer is refused (OSCAR_EINVAL, nothing is launched).
  *   Calls that may overlap need one each. All 16-byte aligned; out may not overlap the inputs.
- * One to seven launches, chosen on the host by the step's lengths: a captured call may be replayed for
+ * Two to nine launches, chosen on the host by the step's lengths (the chunk kernel and its join two,
+ * tiles two more, single tokens over long histories five): a captured call may be replayed for
  * this step only. Runs on the pool's device, which must be current (OSCAR_EINVAL). Errors found by the kernels
  * (a bad page id, a bounded wait) surface from oscar_check. */
 size_t oscar_chunk_workspace_bytes(const oscar_pool* pool);
