@@ -1172,7 +1172,8 @@ __device__ void dequant_role(const ChunkArgs& C, Shared<kDequant>* sh, uint8_t* 
         ok = wait_warp(&sh->code_full[slot], (cpos / slots) & 1, sh, C.err);
         if (!ok) break;
         ++cpos;
-        // this thread's packed words; of a token behind the history the scale and zero are 0, so its values are
+        // This thread's packed words. Of a token behind the history the value's scale and zero are 0, so the values are;
+        // its key is whatever lies there (a page slot that was not loaded, too), and the mask covers its score.
         const uint8_t* kp = codes + (size_t)(slot * 2 + (x >> 6)) * P.block_bytes;
         const uint8_t* vp = codes + (size_t)(slot * 2 + (slice >> 2)) * P.block_bytes;
         const uint4 kc0 = reinterpret_cast<const uint4*>(kp + (x & 63) * kCodeBytes)[0];
