@@ -193,7 +193,6 @@ struct PoolStepView {
   bool in_step, host_only;
   int device;                      // the device the pool's memory lives on
   int64_t* launch_count;
-  const uint8_t* appended;         // per layer: append_and_demote was called in this step
 };
 void pool_step_view(oscar_pool* p, PoolStepView* v);
 

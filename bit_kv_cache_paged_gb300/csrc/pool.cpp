@@ -294,7 +294,6 @@ void oscar::pool_step_view(oscar_pool* p, PoolStepView* v) {
   v->host_only = p->host_only;
   v->device = p->device;
   v->launch_count = &p->launch_count;
-  v->appended = p->appended.data();
 }
 
 extern "C" {
