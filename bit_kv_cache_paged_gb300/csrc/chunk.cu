@@ -888,10 +888,11 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MODE>* sh, uint8_t* sq, 
       }
       // The maximum is taken anew only where it must be: for the rows' first block, and when the weights of
       // 32 (or 128) scores under the last one sum to more than kGrown (each is finite then, or their sum infinite).
-      // The weights already made are scaled then, as the sums and O are. The loops stay rolled: the warps'
+      // The weights already made are scaled then, as the sums and O are. The warp goes through it together, but a row
+      // takes its new maximum only where it needs it: its bits do not depend on the other rows, of later tokens among them. The loops stay rolled: the warps'
       // instructions come from one cache, and unrolled they waited for it longer than for their data.
       float2 sum = make_float2(0.f, 0.f);
-      auto grow = [&](int c0) {
+      auto grow = [&](int c0, bool mine) {
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll 1
         for (int c = c0; c < 4; ++c) {
@@ -905,7 +906,7 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MODE>* sh, uint8_t* sq, 
           }
         }
         const float mb = fmaxf(mx0, mx1) * scale - (decltype(half16)::value ? kHeadroom : 0.f);
-        const float mn = fmaxf(m, mb), alpha = mb > m ? fast_exp2(m - mn) : 1.f;
+        const float mn = mine ? fmaxf(m, mb) : m, alpha = mn > m ? fast_exp2(m - mn) : 1.f;
         m = mn;
         l *= alpha;
         sum.x *= alpha;
@@ -937,15 +938,15 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MODE>* sh, uint8_t* sq, 
           }
         }
       };
-      bool fresh = __any_sync(0xffffffffu, m == -INFINITY);
+      bool mine = m == -INFINITY, renewed = false;  // this row: needs a maximum; has taken it in this block
       const float2 sc2 = make_float2(scale, scale);
       if constexpr (MODE == kDequant) {
-        bool again = fresh;
+        bool again = __any_sync(0xffffffffu, mine);
 #pragma unroll 1
         for (int c = 0;;) {
           if (again) {
-            grow(c);
-            fresh = true;
+            grow(c, mine);
+            renewed |= mine;
             again = false;
           }
           const float nm = m == -INFINITY ? 0.f : -m;
@@ -966,7 +967,8 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MODE>* sh, uint8_t* sq, 
               p[i] = pack2<decltype(half16)::value>(e.x, e.y);
             }
             s0 = __fadd2_rn(s0, s1);
-            again = !fresh && __any_sync(0xffffffffu, s0.x + s0.y > kGrown);
+            mine = !renewed && s0.x + s0.y > kGrown;
+            again = __any_sync(0xffffffffu, mine);
             if (again) break;
             sum = __fadd2_rn(sum, s0);
             tc_st16(tS + 16 * c, p);  // the columns of scores already read
@@ -975,8 +977,9 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MODE>* sh, uint8_t* sq, 
         }
       } else {
         uint32_t p[64];
-        for (;; fresh = true) {
-          if (fresh) grow(0);
+        for (bool again = __any_sync(0xffffffffu, mine);;) {
+          if (again) grow(0, mine);
+          renewed |= mine;
           const float nm = m == -INFINITY ? 0.f : -m;
           const float2 nm2 = make_float2(nm, nm);
           float2 s0 = make_float2(0.f, 0.f), s1 = s0;
@@ -997,7 +1000,9 @@ __device__ void softmax_role(const ChunkArgs& C, Shared<MODE>* sh, uint8_t* sq, 
             }
           }
           sum = __fadd2_rn(s0, s1);
-          if (fresh || !__any_sync(0xffffffffu, sum.x + sum.y > kGrown)) break;
+          mine = !renewed && sum.x + sum.y > kGrown;
+          again = __any_sync(0xffffffffu, mine);
+          if (!again) break;
         }
         tc_st64(tS, p);
       }

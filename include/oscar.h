@@ -233,7 +233,7 @@ oscar_status oscar_step_graph(oscar_pool* pool, const void* k_new_bf16, const vo
  * bf16 outputs 0.0019 where their own rounding alone makes 0.0017). Single tokens over long histories go through
  * the kernels of oscar_decode, which keep 16 or more bits of each (0.0017). Which of the two a sequence's single token takes,
  * and in which order its sums are made, depends on the whole step: the same step gives the same bits, the same
- * sequence beside others may differ by these roundings.
+ * sequence beside others may differ by these roundings. What later tokens hold does not reach a token's bits.
  *   q: dev bf16 [sum(n_new)][num_q_heads][128]; k_new, v_new: dev bf16 [sum(n_new)][num_kv_heads][128],
  *   rows as for oscar_append_and_demote; out: dev bf16, shape of q; workspace: dev scratch of
  *   workspace_bytes bytes, how many depends on the step. oscar_chunk_workspace_bytes(pool) includes room for
@@ -368,7 +368,7 @@ oscar_status oscar_bf16_decode(int32_t num_q_heads, int32_t num_kv_heads, int32_
  * Scores, softmax statistics and sums are fp32; the softmax weights enter the value product in
  * bf16, where oscar_bf16_decode keeps two halves (relative error of the bf16 outputs 0.0020 to 0.0024; their own rounding
  * alone makes 0.0017). The same batch gives the same bits; a sequence's sums are made in an order that depends
- * on the batch. Asynchronous on `stream`; allocates nothing. */
+ * on the batch's lengths. What later tokens hold does not reach a token's bits. Asynchronous on `stream`; allocates nothing. */
 size_t oscar_bf16_chunk_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t n_seqs,
                                         int32_t n_tokens);
 oscar_status oscar_bf16_chunk(int32_t num_q_heads, int32_t num_kv_heads, int32_t n_seqs,
