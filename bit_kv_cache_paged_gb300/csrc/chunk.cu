@@ -43,13 +43,14 @@
 // copies (half of their bytes left out change nothing) and not shared memory (products alone run at
 // their full rate beside them). Beside that an item costs 6000 cycles a tile for queries, masked blocks
 // and output. With codes dequantised in the kernel a block takes 3800 cycles, the expansion.
-// Measured (GB300, 32 query and 8 KV heads unless said; products counted for visible keys only):
-//   8192 new tokens                             362 us, 1520 TFLOP/s
-//   1024 new after 64K, 64 query heads          1490 to 1640 us, 1350 to 1490 TFLOP/s (the power limit's clock)
-//   12 sequences of 1 to 257 after up to 8K     144 us (up to 185 behind work that has drawn the clock down)
-//   16 sequences of 4 after 1K to 32K           177 us, 6620 GB/s: memory bound, 97% of the copy peak
-//   pool, 2048 new after 30000 of INT2          705 us, 1480 TFLOP/s, of it 21 us for the tiles
-//   pool, 10 of 1 to 300 after up to 6K, 64 query heads, group 32      256 us, of it 23 us for the tiles
+// Measured (GB300, 32 query and 8 KV heads unless said; products counted for visible keys only), replayed from a graph ten
+// at a time, and in calls one after another, which draw the clock down:
+//   8192 new tokens                             369 us, 1490 TFLOP/s; 393 a call
+//   1024 new after 64K, 64 query heads          1358 us, 1630 TFLOP/s; 1540 to 1680 a call (the power limit's clock)
+//   12 sequences of 1 to 257 after up to 8K     142 us; 157 a call
+//   16 sequences of 4 after 1K to 32K           175 us, 6700 GB/s: memory bound, 99% of the copy peak; 181 a call
+//   pool, 2048 new after 30000 of INT2          705 us, 1480 TFLOP/s, of it 21 us for the tiles; 775 a call
+//   pool, 10 of 1 to 300 after up to 6K, 64 query heads, group 32      259 us, of it 23 us for the tiles; 264 a call
 //
 // Keys no row may see, and what lies behind a sequence's last key, must not reach a sum even as 0 *
 // NaN: such values are zeroed in shared memory before the product. Where some rows of the tile see

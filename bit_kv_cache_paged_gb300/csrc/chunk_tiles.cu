@@ -10,8 +10,8 @@
 // r * 128, its 16-byte chunk c at chunk position c ^ (r & 7). A CTA expands a block's K (warps 0-3) and V
 // (warps 4-7) into shared memory and sends them out by bulk copies; memory bounds it.
 //
-// Measured: 29700 tokens of 8 KV heads, group 128 (139 MB read and written) 21 us, 6600 GB/s; the chunk that follows
-// (2048 tokens) takes 680 us where dequantising in the kernel took 897.
+// Measured: 29700 tokens of 8 KV heads, group 128 (139 MB read and written) 21 us, 6600 GB/s; the whole call
+// of 2048 tokens, replayed from a graph, 705 us, where dequantising in the kernel takes 893.
 #include <type_traits>
 
 #include "int2_tiles.cuh"
