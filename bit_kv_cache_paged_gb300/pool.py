@@ -169,7 +169,7 @@ class Pool:
             except torch.cuda.OutOfMemoryError:
                 workspace = torch.empty(max(lib.oscar_chunk_workspace_min_bytes(self.handle), 16), dtype=torch.uint8, device=q.device)
         else:
-            _need(workspace, torch.uint8, workspace.shape, "workspace")
+            _need(workspace, torch.uint8, getattr(workspace, "shape", ()), "workspace")
             if not _on_current_device(workspace):
                 raise ValueError("workspace must be on the current CUDA device")
         B._check("oscar_chunk_attend", lib.oscar_chunk_attend(self.handle, layer, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),

@@ -119,8 +119,10 @@ def test_workspace_argument_is_checked():
     for bad in (torch.empty(n, dtype=torch.uint8), torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2]):
         with pytest.raises(ValueError):
             m.pool.chunk_attend(0, q, k, v, workspace=bad)
-    with pytest.raises(TypeError):
-        m.pool.chunk_attend(0, q, k, v, workspace=torch.empty(n, dtype=torch.int8, device="cuda"))
+    for bad in (torch.empty(n, dtype=torch.int8, device="cuda"), 1 << 20):
+        with pytest.raises(TypeError):
+            m.pool.chunk_attend(0, q, k, v, workspace=bad)
+    refused(lambda: m.pool.chunk_attend(0, q, k, v, workspace=torch.empty(n + 8, dtype=torch.uint8, device="cuda")[8:]))  # alignment
 
 
 def test_tiles_stay_within_their_limit():
